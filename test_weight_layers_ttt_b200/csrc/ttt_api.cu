@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "api_common.h"
 #include "gemm.h"
 #include "ops.h"
 
@@ -55,39 +56,61 @@ unsigned long long wait_limit_ns() {
   return kDefaultWaitNs;
 }
 
-namespace {
-
-// ------------------------------------------------------------------ kernel tracing
-struct TraceState {
-  std::mutex mu;
-  bool on = false;
-  int dev = -1;
-  int n = 0;
-  int cap = 0;
-  std::vector<cudaEvent_t> ev;  // 2 per record
-  std::vector<const char*> names;
-};
+// The state behind api_common.h.
 TraceState g_trace;
+std::atomic<int> g_checks{0};
+thread_local std::vector<unsigned*> t_guards;
 
-// Brackets one kernel launch with two events on its stream while tracing is enabled.
-struct TraceScope {
-  int idx = -1;
-  cudaStream_t s;
-  TraceScope(const char* name, cudaStream_t st) : s(st) {
-    if (!g_trace.on) return;
-    std::lock_guard<std::mutex> lk(g_trace.mu);
-    int d = -1;
-    if (!g_trace.on || cudaGetDevice(&d) != cudaSuccess || d != g_trace.dev ||
-        g_trace.n >= g_trace.cap)
-      return;
-    idx = g_trace.n++;
-    g_trace.names[idx] = name;
-    cudaEventRecord(g_trace.ev[2 * idx], s);
+ttt_status fail(ttt_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+ttt_status run_guards(bool check, cudaStream_t s) {
+  for (size_t i0 = 0; i0 < t_guards.size(); i0 += kMaxGuards) {
+    GuardList g;
+    g.n = (int)std::min<size_t>(kMaxGuards, t_guards.size() - i0);
+    for (int i = 0; i < g.n; ++i) g.p[i] = t_guards[i0 + i];
+    TraceScope ts(check ? "guards_check" : "guards_fill", s);
+    const cudaError_t e = check ? guards_check(g, device_error_word(), s) : guards_fill(g, s);
+    if (e != cudaSuccess)
+      return fail(TTT_ERR_CUDA, "debug guards: %s", cudaGetErrorString(e));
   }
-  ~TraceScope() {
-    if (idx >= 0) cudaEventRecord(g_trace.ev[2 * idx + 1], s);
-  }
-};
+  return TTT_OK;
+}
+
+ttt_status checks_begin(cudaStream_t s) {
+  if (!(g_checks.load() & TTT_CHECK_GUARDS)) return TTT_OK;
+  return run_guards(false, s);
+}
+
+ttt_status checks_end(cudaStream_t s, std::initializer_list<OutBuf> outs) {
+  const int f = g_checks.load();
+  if (f & TTT_CHECK_GUARDS) TTT_TRY(run_guards(true, s));
+  if (f & TTT_CHECK_FINITE)
+    for (const OutBuf& o : outs) {
+      if (!o.p || o.n <= 0) continue;
+      TraceScope ts("finite_scan", s);
+      const cudaError_t e = finite_scan(o.dt, o.p, o.n, device_error_word(), s);
+      if (e != cudaSuccess) return fail(TTT_ERR_CUDA, "finite scan: %s", cudaGetErrorString(e));
+    }
+  return TTT_OK;
+}
+
+ttt_status check_ws(void* ws, size_t have, size_t need) {
+  if (need == 0) return TTT_OK;
+  if (!ws) return fail(TTT_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
+  if (reinterpret_cast<uintptr_t>(ws) & 255)
+    return fail(TTT_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (have < need)
+    return fail(TTT_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
+  return TTT_OK;
+}
+
+namespace {
 
 // "<name>@<engine>" with stable storage, for trace records.
 const char* engine_name(const char* name, const char* engine) {
@@ -99,8 +122,6 @@ const char* engine_name(const char* name, const char* engine) {
   if (it == names.end()) it = names.emplace(key, key).first;
   return it->second.c_str();
 }
-
-ttt_status fail(ttt_status st, const char* fmt, ...);
 
 // One contraction. bf16 operands (bf16 mode) run on the tcgen05 tensor-core engine only: a
 // problem that engine cannot take is refused with TTT_ERR_UNSUPPORTED, never rerouted.
@@ -133,120 +154,6 @@ ttt_status run_simt(const char* name, const GemmProblem& p, cudaStream_t s) {
   if (p.M <= 0 || p.N <= 0 || p.Z0 <= 0 || p.Z1 <= 0) return TTT_OK;
   TraceScope ts(g_trace.on ? engine_name(name, "simt") : name, s);
   return gemm_simt(p, s);
-}
-
-#define TTT_TRY(expr)                        \
-  do {                                       \
-    ttt_status st__ = (expr);                \
-    if (st__ != TTT_OK) return st__;         \
-  } while (0)
-
-#define TTT_CUDA(expr)                                                                    \
-  do {                                                                                    \
-    cudaError_t e__ = (expr);                                                             \
-    if (e__ != cudaSuccess) {                                                             \
-      set_error_message("%s failed: %s", #expr, cudaGetErrorString(e__));                 \
-      return TTT_ERR_CUDA;                                                                \
-    }                                                                                     \
-  } while (0)
-
-// One traced kernel launch of ops.h.
-#define TTT_OP(name, expr)         \
-  do {                             \
-    TraceScope ts__((name), s);    \
-    TTT_CUDA(expr);                \
-  } while (0)
-
-ttt_status fail(ttt_status st, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
-  va_end(ap);
-  return st;
-}
-
-bool al16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// ------------------------------------------------------------------ debug checks
-// Process-wide TTT_CHECK_* flags (ttt_set_debug_checks), and the guards the calling thread's
-// current call carved from its workspace.
-std::atomic<int> g_checks{0};
-thread_local std::vector<unsigned*> t_guards;
-
-// Bump allocator over the caller's workspace (or a size counter when base is null). With
-// TTT_CHECK_GUARDS on, a kGuardBytes guard sits in front of the first region and right
-// after the end of every region (16-byte aligned); the guards of a real workspace are
-// listed in t_guards.
-struct Carve {
-  char* base;
-  size_t off = 0;
-  bool guards;
-  explicit Carve(void* b)
-      : base(static_cast<char*>(b)), guards((g_checks.load() & TTT_CHECK_GUARDS) != 0) {
-    if (guards) guard();
-  }
-  void guard() {
-    off = (off + 15) & ~static_cast<size_t>(15);
-    if (base) t_guards.push_back(reinterpret_cast<unsigned*>(base + off));
-    off += kGuardBytes;
-  }
-  void* take(size_t bytes) {
-    off = (off + 255) & ~static_cast<size_t>(255);
-    void* p = base ? base + off : nullptr;
-    off += bytes;
-    if (guards) guard();
-    return p;
-  }
-  template <typename T> T* take_n(long long n) { return static_cast<T*>(take(sizeof(T) * (size_t)n)); }
-};
-
-// Fills (check = false) or compares (check = true) every guard in t_guards.
-ttt_status run_guards(bool check, cudaStream_t s) {
-  for (size_t i0 = 0; i0 < t_guards.size(); i0 += kMaxGuards) {
-    GuardList g;
-    g.n = (int)std::min<size_t>(kMaxGuards, t_guards.size() - i0);
-    for (int i = 0; i < g.n; ++i) g.p[i] = t_guards[i0 + i];
-    TraceScope ts(check ? "guards_check" : "guards_fill", s);
-    const cudaError_t e = check ? guards_check(g, device_error_word(), s) : guards_fill(g, s);
-    if (e != cudaSuccess)
-      return fail(TTT_ERR_CUDA, "debug guards: %s", cudaGetErrorString(e));
-  }
-  return TTT_OK;
-}
-
-// One output of a call, for the non-finite scan.
-struct OutBuf {
-  const void* p;
-  long long n;
-  int dt;
-};
-
-// Start of a call's work on `s`: writes the guards of the workspace just planned.
-ttt_status checks_begin(cudaStream_t s) {
-  if (!(g_checks.load() & TTT_CHECK_GUARDS)) return TTT_OK;
-  return run_guards(false, s);
-}
-
-// End of a call's work on `s`: compares the guards and scans the outputs.
-ttt_status checks_end(cudaStream_t s, std::initializer_list<OutBuf> outs) {
-  const int f = g_checks.load();
-  if (f & TTT_CHECK_GUARDS) TTT_TRY(run_guards(true, s));
-  if (f & TTT_CHECK_FINITE)
-    for (const OutBuf& o : outs) {
-      if (!o.p || o.n <= 0) continue;
-      TraceScope ts("finite_scan", s);
-      const cudaError_t e = finite_scan(o.dt, o.p, o.n, device_error_word(), s);
-      if (e != cudaSuccess) return fail(TTT_ERR_CUDA, "finite scan: %s", cudaGetErrorString(e));
-    }
-  return TTT_OK;
-}
-
-// A call's body between checks_begin and checks_end; the end runs after a successful body.
-template <typename F>
-ttt_status with_checks(cudaStream_t s, std::initializer_list<OutBuf> outs, F&& body) {
-  TTT_TRY(checks_begin(s));
-  TTT_TRY(body());
-  return checks_end(s, outs);
 }
 
 ttt_status check_desc(const ttt_desc* d, int path) {
@@ -1206,16 +1113,6 @@ ttt_status rec_update(const ttt_desc& d, const void* k, const void* v, const flo
                                     (int)BH, d.H, d.h, d.m, mask, d.sign, d.renorm, b.Wk[bout],
                                     b.W1t[bout], ot, s));
   }
-  return TTT_OK;
-}
-
-ttt_status check_ws(void* ws, size_t have, size_t need) {
-  if (need == 0) return TTT_OK;
-  if (!ws) return fail(TTT_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
-  if (reinterpret_cast<uintptr_t>(ws) & 255)
-    return fail(TTT_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  if (have < need)
-    return fail(TTT_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
   return TTT_OK;
 }
 
