@@ -348,6 +348,183 @@ ttt_status ttt_lm_target(int32_t N, int32_t d, const void* X0, const float* conv
                          const void* W_target, void* vbar, void* workspace,
                          size_t workspace_bytes, ttt_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * The token mixer around the layer: the operators in front of it (a short causal
+ * convolution, the head norm with position rotation that makes its q and k) and the gated
+ * recurrent form beside linear attention (the selective state space scan). No counterpart in
+ * the pages beyond the normalised q, k and the causal convolution that they take as given.
+ * Each has its forward for prompts, its backward for training and a form for single tokens.
+ *
+ * Tensors are token-major: [B, N, D] with the elements of a token contiguous. The inputs may
+ * be slices of a wider buffer (a fused projection): a *_row field of the descriptor is the
+ * distance in elements between two tokens (0: dense); sequence b starts N rows after
+ * sequence b - 1. Outputs and gradients are dense. Any size and element alignment is taken;
+ * 16-byte aligned rows of whole 16-byte runs are the fast case.
+ *
+ * lens (nullable, [B] int32 on the device): tokens of each sequence, clamped to 0..N. Tokens
+ * behind a sequence's end are not read, their outputs and gradients are written as zeros, and
+ * the state is the one after the sequence's last token.
+ *
+ * Outputs may not overlap inputs or one another, except that a forward's state_out may be its
+ * state_in. Sums, norms, states and all elementwise math are fp32; 16-bit outputs are rounded
+ * once. Results are the same on every call with the same arguments (no atomics). Nothing is
+ * kept between calls; the calls can be captured into a CUDA graph. Errors, streams and
+ * ownership as for the rest of the library; the debug checks cover these calls too
+ * (ttt_debug_check_workspace excepted, which takes a ttt_desc).
+ * ------------------------------------------------------------------------------------ */
+enum { TTT_ACT_NONE = 0, TTT_ACT_SILU = 1 };
+enum { TTT_NORM_NONE = 0, TTT_NORM_RMS = 1, TTT_NORM_L2 = 2 };
+enum { TTT_PAIRS_HALVES = 0, TTT_PAIRS_INTERLEAVED = 1 };
+
+typedef struct ttt_conv_desc {
+  int32_t B, N;      /* sequences and tokens, >= 0; B <= 65535, N <= 4194304, B*N < 2^31 */
+  int32_t D;         /* channels, 1..1048576 */
+  int32_t width;     /* taps, 2..8 */
+  int32_t dtype;     /* TTT_DTYPE_* of x, y, the state and their gradients */
+  int32_t act;       /* TTT_ACT_* */
+  int64_t x_row;     /* elements between tokens of x (0: D) */
+} ttt_conv_desc;
+
+/*
+ * Short causal depthwise convolution:
+ *     y[t] = act(bias + sum_{j < width} w[j] * x[t - j]),
+ * where x[-1], x[-2], ... are the state: the last width - 1 inputs, oldest first.
+ *
+ *   x          [B,N,D] dtype, rows x_row apart
+ *   w          [width,D] fp32 taps (tap j multiplies x[t - j])
+ *   bias       nullable [D] fp32
+ *   state_in   nullable [B,width-1,D] dtype (NULL: zeros)
+ *   lens       nullable [B]
+ *   y          [B,N,D] dtype, written
+ *   state_out  nullable [B,width-1,D] dtype, written; may be state_in
+ */
+ttt_status ttt_short_conv_fwd(const ttt_conv_desc* desc, const void* x, const float* w,
+                              const float* bias, const void* state_in, const int32_t* lens,
+                              void* y, void* state_out, ttt_stream_t stream);
+
+/*
+ * The next token of B sequences (desc->N = 1): x [B,D] (rows x_row apart), y [B,D], state
+ * [B,width-1,D] read and shifted in place.
+ */
+ttt_status ttt_short_conv_step(const ttt_conv_desc* desc, const void* x, const float* w,
+                               const float* bias, void* state, void* y, ttt_stream_t stream);
+
+/*
+ * Backward of ttt_short_conv_fwd. The forward inputs, dy [B,N,D] and dstate_out (nullable,
+ * the gradient of state_out) give dx [B,N,D], dw [width,D] fp32, dbias (nullable) [D] fp32 and
+ * dstate_in (nullable) [B,width-1,D]. workspace >=
+ * ttt_short_conv_bwd_workspace_bytes(desc) bytes, 256-byte aligned.
+ */
+size_t ttt_short_conv_bwd_workspace_bytes(const ttt_conv_desc* desc);
+ttt_status ttt_short_conv_bwd(const ttt_conv_desc* desc, const void* x, const float* w,
+                              const float* bias, const void* state_in, const int32_t* lens,
+                              const void* dy, const void* dstate_out, void* dx, float* dw,
+                              float* dbias, void* dstate_in, void* workspace,
+                              size_t workspace_bytes, ttt_stream_t stream);
+
+typedef struct ttt_heads_desc {
+  int32_t B, N;             /* as in ttt_conv_desc */
+  int32_t Hq, Hk, Hv;       /* heads of q, k and v, 0..65535 (0: absent) */
+  int32_t h;                /* head width, 1..512 */
+  int32_t dtype;            /* TTT_DTYPE_* */
+  int32_t norm;             /* TTT_NORM_* of q and k */
+  int32_t rot;              /* rotated elements of q and k, even, 0..h */
+  int32_t pairs;            /* TTT_PAIRS_*: pair p is (p, p + rot/2) or (2p, 2p + 1) */
+  float eps;                /* > 0 with a norm */
+  int32_t pos0;             /* position of token 0 when positions is NULL */
+  int64_t q_row, k_row, v_row;   /* elements between tokens (0: H*h) */
+} ttt_heads_desc;
+
+/*
+ * Norm of every query and key head and the position rotation, in one pass from the
+ * projection's token-major q, k, v [B,N,H,h] to the layer's head-major [B,H,N,h]:
+ *     n = g * x * r,  r = (sum x^2 + eps)^(-1/2)  (TTT_NORM_L2)
+ *                     r = (mean x^2 + eps)^(-1/2) (TTT_NORM_RMS),  r = 1 (TTT_NORM_NONE),
+ *     (a, b) -> (a cos - b sin, b cos + a sin) for each pair p of n's first rot elements,
+ *     with the angle position * inv_freq[p] (taken in 64 bits),
+ * and v only laid out.
+ *
+ *   wq, wk     nullable [h] fp32 norm weights g
+ *   inv_freq   [rot/2] fp32 (rot > 0)
+ *   positions  nullable [B,N] int32; NULL: pos0 + t
+ *   q_out, k_out, v_out  [B,H,N,h], written (one for each tensor with heads)
+ */
+ttt_status ttt_head_norm_rope_fwd(const ttt_heads_desc* desc, const void* q, const void* k,
+                                  const void* v, const float* wq, const float* wk,
+                                  const float* inv_freq, const int32_t* positions, void* q_out,
+                                  void* k_out, void* v_out, ttt_stream_t stream);
+
+/*
+ * Backward: dq_out, dk_out, dv_out [B,H,N,h] give dq, dk, dv [B,N,H,h] (dense) and the weight
+ * gradients dwq, dwk (nullable) [h] fp32. The workspace is needed for a weight gradient only.
+ */
+size_t ttt_head_norm_rope_bwd_workspace_bytes(const ttt_heads_desc* desc);
+ttt_status ttt_head_norm_rope_bwd(const ttt_heads_desc* desc, const void* q, const void* k,
+                                  const float* wq, const float* wk, const float* inv_freq,
+                                  const int32_t* positions, const void* dq_out,
+                                  const void* dk_out, const void* dv_out, void* dq, void* dk,
+                                  void* dv, float* dwq, float* dwk, void* workspace,
+                                  size_t workspace_bytes, ttt_stream_t stream);
+
+typedef struct ttt_scan_desc {
+  int32_t B, N;             /* as in ttt_conv_desc */
+  int32_t D;                /* channels, 1..1048576, B*D < 2^31 */
+  int32_t S;                /* state elements of a channel, 1..64 */
+  int32_t G;                /* groups of D/G channels that share B and C; divides D */
+  int32_t dtype;            /* TTT_DTYPE_* of u, dt, Bm, Cm, z, y and their gradients */
+  int32_t softplus;         /* 1: delta = softplus(dt + dt_bias); 0: delta = dt + dt_bias */
+  int32_t reserved;         /* 0 */
+  int64_t u_row, dt_row, z_row, b_row, c_row;   /* elements between tokens (0: dense) */
+} ttt_scan_desc;
+
+/*
+ * Selective state space scan. For channel d of group g and state element s
+ *     h_t[d,s] = exp(delta_t[d] A[d,s]) h_{t-1}[d,s] + delta_t[d] u_t[d] Bm_t[g,s],
+ *     y_t[d]   = (sum_s Cm_t[g,s] h_t[d,s] + D[d] u_t[d]) * silu(z_t[d]).
+ * A is a decay (<= 0): with growth that leaves fp32's range over a sequence the result is
+ * undefined.
+ *
+ *   u, dt      [B,N,D] dtype
+ *   A          [D,S] fp32
+ *   Bm, Cm     [B,N,G,S] dtype
+ *   D          nullable [D] fp32; z nullable [B,N,D] dtype (NULL: no gate)
+ *   dt_bias    nullable [D] fp32
+ *   state_in   nullable [B,D,S] fp32 (NULL: zeros)
+ *   y          [B,N,D] dtype, written
+ *   state_out  nullable [B,D,S] fp32, written; may be state_in
+ *   workspace  >= ttt_selective_scan_workspace_bytes(desc, 0) bytes, 256-byte aligned (0
+ *              bytes, and NULL allowed, when the sequences need not be split)
+ */
+size_t ttt_selective_scan_workspace_bytes(const ttt_scan_desc* desc, int32_t backward);
+ttt_status ttt_selective_scan_fwd(const ttt_scan_desc* desc, const void* u, const void* dt,
+                                  const float* A, const void* Bm, const void* Cm, const float* D,
+                                  const void* z, const float* dt_bias, const float* state_in,
+                                  const int32_t* lens, void* y, float* state_out,
+                                  void* workspace, size_t workspace_bytes, ttt_stream_t stream);
+
+/*
+ * The next token of B sequences (desc->N = 1): u, dt, z [B,D], Bm, Cm [B,G,S], y [B,D];
+ * state [B,D,S] fp32 is read and written in place.
+ */
+ttt_status ttt_selective_scan_step(const ttt_scan_desc* desc, const void* u, const void* dt,
+                                   const float* A, const void* Bm, const void* Cm, const float* D,
+                                   const void* z, const float* dt_bias, float* state, void* y,
+                                   ttt_stream_t stream);
+
+/*
+ * Backward of ttt_selective_scan_fwd: the forward inputs, dy [B,N,D] and dstate_out (nullable,
+ * the gradient of state_out) give du, ddt [B,N,D], dA [D,S] fp32, dBm, dCm [B,N,G,S], dz (with
+ * z) [B,N,D], and dD, ddt_bias (nullable) [D] and dstate_in (nullable) [B,D,S] fp32. The
+ * states are recomputed. workspace >= ttt_selective_scan_workspace_bytes(desc, 1) bytes.
+ */
+ttt_status ttt_selective_scan_bwd(const ttt_scan_desc* desc, const void* u, const void* dt,
+                                  const float* A, const void* Bm, const void* Cm, const float* D,
+                                  const void* z, const float* dt_bias, const float* state_in,
+                                  const int32_t* lens, const void* dy, const float* dstate_out,
+                                  void* du, void* ddt, float* dA, void* dBm, void* dCm, float* dD,
+                                  void* dz, float* ddt_bias, float* dstate_in, void* workspace,
+                                  size_t workspace_bytes, ttt_stream_t stream);
+
 /*
  * Synchronises `stream`, then reads and clears the device error word of the current
  * device: TTT_OK, TTT_ERR_TIMEOUT (a bounded wait ran out) or TTT_ERR_DEVICE (a debug

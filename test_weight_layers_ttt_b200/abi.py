@@ -38,6 +38,13 @@ TTT_PATH_LINEAR = 2
 TTT_PATH_PARALLEL_MOMENTUM = 3
 TTT_PATH_PARALLEL_BWD = 4
 TTT_STATIC_SCRATCH_BYTES = 64 << 20
+TTT_ACT_NONE = 0
+TTT_ACT_SILU = 1
+TTT_NORM_NONE = 0
+TTT_NORM_RMS = 1
+TTT_NORM_L2 = 2
+TTT_PAIRS_HALVES = 0
+TTT_PAIRS_INTERLEAVED = 1
 TTT_CHECK_GUARDS = 1
 TTT_CHECK_FINITE = 2
 
@@ -47,7 +54,11 @@ EXPORTED = (
     "ttt_la_parallel_fwd_shard", "ttt_la_parallel_fwd_shard_outputs",
     "ttt_linear_attn_fwd", "ttt_la_parallel_momentum_fwd", "ttt_la_parallel_bwd",
     "ttt_lact_recurrent_fwd",
-    "ttt_lm_target_workspace_bytes", "ttt_lm_target", "ttt_last_device_status",
+    "ttt_lm_target_workspace_bytes", "ttt_lm_target",
+    "ttt_short_conv_fwd", "ttt_short_conv_step", "ttt_short_conv_bwd_workspace_bytes",
+    "ttt_short_conv_bwd", "ttt_head_norm_rope_fwd", "ttt_head_norm_rope_bwd_workspace_bytes",
+    "ttt_head_norm_rope_bwd", "ttt_selective_scan_workspace_bytes", "ttt_selective_scan_fwd",
+    "ttt_selective_scan_step", "ttt_selective_scan_bwd", "ttt_last_device_status",
     "ttt_set_debug_checks", "ttt_get_debug_checks", "ttt_debug_check_workspace",
     "ttt_debug_wait_timeout", "ttt_trace_enable", "ttt_trace_disable", "ttt_trace_count",
     "ttt_trace_get", "ttt_status_str", "ttt_last_error_message", "ttt_version",
@@ -71,6 +82,24 @@ class ttt_desc(ctypes.Structure):
 
     def __repr__(self):
         return "ttt_desc(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class ttt_conv_desc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("B", "N", "D", "width", "dtype", "act")] + \
+        [("x_row", ctypes.c_int64)]
+
+
+class ttt_heads_desc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "B", "N", "Hq", "Hk", "Hv", "h", "dtype", "norm", "rot", "pairs")] + \
+        [("eps", ctypes.c_float), ("pos0", ctypes.c_int32)] + \
+        [(name, ctypes.c_int64) for name in ("q_row", "k_row", "v_row")]
+
+
+class ttt_scan_desc(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "B", "N", "D", "S", "G", "dtype", "softplus", "reserved")] + \
+        [(name, ctypes.c_int64) for name in ("u_row", "dt_row", "z_row", "b_row", "c_row")]
 
 
 _lib = None
@@ -108,6 +137,29 @@ def lib() -> ctypes.CDLL:
         L.ttt_lm_target_workspace_bytes.restype = S
         L.ttt_lm_target.argtypes = [I32, I32, P, P, P, P, P, S, P]
         L.ttt_lm_target.restype = I32
+        DC, DH, DS = (ctypes.POINTER(t) for t in (ttt_conv_desc, ttt_heads_desc, ttt_scan_desc))
+        L.ttt_short_conv_fwd.argtypes = [DC] + [P] * 8
+        L.ttt_short_conv_fwd.restype = I32
+        L.ttt_short_conv_step.argtypes = [DC] + [P] * 6
+        L.ttt_short_conv_step.restype = I32
+        L.ttt_short_conv_bwd_workspace_bytes.argtypes = [DC]
+        L.ttt_short_conv_bwd_workspace_bytes.restype = S
+        L.ttt_short_conv_bwd.argtypes = [DC] + [P] * 12 + [S, P]
+        L.ttt_short_conv_bwd.restype = I32
+        L.ttt_head_norm_rope_fwd.argtypes = [DH] + [P] * 11
+        L.ttt_head_norm_rope_fwd.restype = I32
+        L.ttt_head_norm_rope_bwd_workspace_bytes.argtypes = [DH]
+        L.ttt_head_norm_rope_bwd_workspace_bytes.restype = S
+        L.ttt_head_norm_rope_bwd.argtypes = [DH] + [P] * 15 + [S, P]
+        L.ttt_head_norm_rope_bwd.restype = I32
+        L.ttt_selective_scan_workspace_bytes.argtypes = [DS, I32]
+        L.ttt_selective_scan_workspace_bytes.restype = S
+        L.ttt_selective_scan_fwd.argtypes = [DS] + [P] * 13 + [S, P]
+        L.ttt_selective_scan_fwd.restype = I32
+        L.ttt_selective_scan_step.argtypes = [DS] + [P] * 11
+        L.ttt_selective_scan_step.restype = I32
+        L.ttt_selective_scan_bwd.argtypes = [DS] + [P] * 22 + [S, P]
+        L.ttt_selective_scan_bwd.restype = I32
         L.ttt_last_device_status.argtypes = [P]
         L.ttt_last_device_status.restype = I32
         L.ttt_set_debug_checks.argtypes = [I32]
@@ -256,6 +308,80 @@ def ttt_lm_target(N, d, X0, conv_w, W_target, vbar, workspace, workspace_bytes=N
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     _check(lib().ttt_lm_target(N, d, _ptr(X0), _ptr(conv_w), _ptr(W_target), _ptr(vbar),
                                _ptr(workspace), wb, _stream(stream)))
+
+
+def ttt_short_conv_fwd(desc, x, w, bias, state_in, lens, y, state_out, stream=None):
+    _check(lib().ttt_short_conv_fwd(
+        ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(state_in), _ptr(lens), _ptr(y),
+        _ptr(state_out), _stream(stream)))
+
+
+def ttt_short_conv_step(desc, x, w, bias, state, y, stream=None):
+    _check(lib().ttt_short_conv_step(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias),
+                                     _ptr(state), _ptr(y), _stream(stream)))
+
+
+def ttt_short_conv_bwd_workspace_bytes(desc) -> int:
+    return int(lib().ttt_short_conv_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def ttt_short_conv_bwd(desc, x, w, bias, state_in, lens, dy, dstate_out, dx, dw, dbias,
+                       dstate_in, workspace, workspace_bytes=None, stream=None):
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _check(lib().ttt_short_conv_bwd(
+        ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(state_in), _ptr(lens), _ptr(dy),
+        _ptr(dstate_out), _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dstate_in), _ptr(workspace), wb,
+        _stream(stream)))
+
+
+def ttt_head_norm_rope_fwd(desc, q, k, v, wq, wk, inv_freq, positions, q_out, k_out, v_out,
+                           stream=None):
+    _check(lib().ttt_head_norm_rope_fwd(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(wq), _ptr(wk), _ptr(inv_freq),
+        _ptr(positions), _ptr(q_out), _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def ttt_head_norm_rope_bwd_workspace_bytes(desc) -> int:
+    return int(lib().ttt_head_norm_rope_bwd_workspace_bytes(ctypes.byref(desc)))
+
+
+def ttt_head_norm_rope_bwd(desc, q, k, wq, wk, inv_freq, positions, dq_out, dk_out, dv_out, dq,
+                           dk, dv, dwq, dwk, workspace, workspace_bytes=None, stream=None):
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _check(lib().ttt_head_norm_rope_bwd(
+        ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(inv_freq),
+        _ptr(positions), _ptr(dq_out), _ptr(dk_out), _ptr(dv_out), _ptr(dq), _ptr(dk), _ptr(dv),
+        _ptr(dwq), _ptr(dwk), _ptr(workspace), wb, _stream(stream)))
+
+
+def ttt_selective_scan_workspace_bytes(desc, backward: int) -> int:
+    return int(lib().ttt_selective_scan_workspace_bytes(ctypes.byref(desc), int(backward)))
+
+
+def ttt_selective_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state_in, lens, y, state_out,
+                           workspace, workspace_bytes=None, stream=None):
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _check(lib().ttt_selective_scan_fwd(
+        ctypes.byref(desc), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+        _ptr(dt_bias), _ptr(state_in), _ptr(lens), _ptr(y), _ptr(state_out), _ptr(workspace), wb,
+        _stream(stream)))
+
+
+def ttt_selective_scan_step(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, y, stream=None):
+    _check(lib().ttt_selective_scan_step(
+        ctypes.byref(desc), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+        _ptr(dt_bias), _ptr(state), _ptr(y), _stream(stream)))
+
+
+def ttt_selective_scan_bwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state_in, lens, dy, dstate_out,
+                           du, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dstate_in, workspace,
+                           workspace_bytes=None, stream=None):
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _check(lib().ttt_selective_scan_bwd(
+        ctypes.byref(desc), _ptr(u), _ptr(dt), _ptr(A), _ptr(Bm), _ptr(Cm), _ptr(D), _ptr(z),
+        _ptr(dt_bias), _ptr(state_in), _ptr(lens), _ptr(dy), _ptr(dstate_out), _ptr(du),
+        _ptr(ddt), _ptr(dA), _ptr(dBm), _ptr(dCm), _ptr(dD), _ptr(dz), _ptr(ddt_bias),
+        _ptr(dstate_in), _ptr(workspace), wb, _stream(stream)))
 
 
 def ttt_last_device_status(stream=None):

@@ -1,0 +1,371 @@
+// The short causal depthwise convolution: pre[t] = bias + sum_j w[j] x[t - j] for width 2..8
+// taps, y = pre or silu(pre), with the last width - 1 inputs as the state of a sequence.
+//
+// HBM bound: a token costs one read and one write of its channels forward, two reads and one
+// write backward. A thread owns V consecutive channels over a run of tokens and slides the
+// window through registers, so a row is read once per run (plus width - 1 halo rows) and every
+// access of the vector form is 8 or 16 bytes. The next kAhead rows are loaded before the
+// current ones are used: bytes in flight, not arithmetic, set the rate.
+#include "mixer.h"
+#include "mixer_common.cuh"
+
+namespace ttt {
+namespace {
+
+constexpr int kConvThreads = 128;
+constexpr int kAhead = 4;    // rows loaded together
+
+__device__ __forceinline__ int sequence_length(const int* lens, int b, int N) {
+  return lens ? min(max(lens[b], 0), N) : N;
+}
+
+// Row `i` of the inputs with the state in front of them (row width - 1 is token 0).
+template <typename T, int V, int K>
+__device__ __forceinline__ void history_row(const ConvArgs& a, int b, int c, long long i,
+                                            float (&f)[V]) {
+  if (i >= K - 1) {
+    load_vec<T, V>(static_cast<const T*>(a.x) +
+                       ((long long)b * a.N + i - (K - 1)) * a.x_row + c, f);
+  } else if (a.state_in) {
+    load_vec<T, V>(static_cast<const T*>(a.state_in) + ((long long)b * (K - 1) + i) * a.D + c, f);
+  } else {
+#pragma unroll
+    for (int q = 0; q < V; ++q) f[q] = 0.0f;
+  }
+}
+
+// V fp32 parameters, aligned or not.
+template <int V>
+__device__ __forceinline__ void load_params(const float* p, float (&f)[V]) {
+#pragma unroll
+  for (int q = 0; q < V; ++q) f[q] = p[q];
+}
+
+// grid (channel blocks * runs, B): the channel blocks of one run are neighbours.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int cblocks, int run) {
+  const int c = ((blockIdx.x % cblocks) * kConvThreads + threadIdx.x) * V;
+  if (c >= a.D) return;
+  const int b = blockIdx.y;
+  const int t0 = (int)(blockIdx.x / cblocks) * run;
+  const int t1 = min(a.N, t0 + run);
+  const int n = sequence_length(a.lens, b, a.N);
+  T* y = static_cast<T*>(a.y) + (long long)b * a.N * a.D + c;
+  const T* x = static_cast<const T*>(a.x) + (long long)b * a.N * a.x_row + c;
+  float w[K][V], bias[V];
+#pragma unroll
+  for (int j = 0; j < K; ++j) load_params<V>(a.w + (long long)j * a.D + c, w[j]);
+#pragma unroll
+  for (int q = 0; q < V; ++q) bias[q] = a.bias ? a.bias[c + q] : 0.0f;
+
+  if (t0 < n) {
+    float win[K - 1][V];   // win[j - 1] = x[t - j]
+#pragma unroll
+    for (int j = 1; j < K; ++j) history_row<T, V, K>(a, b, c, (long long)t0 - j + K - 1, win[j - 1]);
+    const int te = min(t1, n);
+    for (int t = t0; t < te; t += kAhead) {
+      typename Pack<T, V>::U raw[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (t + i < te) raw[i] = load_raw<T, V>(x + (long long)(t + i) * a.x_row);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (t + i >= te) break;
+        float cur[V], o[V];
+        unpack<T, V>(raw[i], cur);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          float acc = fmaf(w[0][q], cur[q], bias[q]);
+#pragma unroll
+          for (int j = 1; j < K; ++j) acc = fmaf(w[j][q], win[j - 1][q], acc);
+          o[q] = a.act ? acc * fast_sigmoid(acc) : acc;
+        }
+        store_vec<T, V>(y + (long long)(t + i) * a.D, o);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+#pragma unroll
+          for (int j = K - 2; j > 0; --j) win[j][q] = win[j - 1][q];
+          win[0][q] = cur[q];
+        }
+      }
+    }
+  }
+  // rows behind the sequence's end
+  const float zero[V] = {};
+  for (int t = max(t0, n); t < t1; ++t) store_vec<T, V>(y + (long long)t * a.D, zero);
+  // the state: rows n .. n + K - 2 of the history. This thread is the only one that reads
+  // its channels' state, and row i is written after row n + i was read, so state_out may be
+  // state_in.
+  if (a.state_out && t0 == 0) {
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) {
+      float f[V];
+      history_row<T, V, K>(a, b, c, (long long)n + i, f);
+      store_vec<T, V>(static_cast<T*>(a.state_out) + ((long long)b * (K - 1) + i) * a.D + c, f);
+    }
+  }
+}
+
+// One token per sequence, the state shifted in place. grid (channel blocks, B).
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a) {
+  const int c = (blockIdx.x * kConvThreads + threadIdx.x) * V;
+  if (c >= a.D) return;
+  const int b = blockIdx.y;
+  T* st = static_cast<T*>(a.state_out) + (long long)b * (K - 1) * a.D + c;
+  typename Pack<T, V>::U raw[K];   // oldest first
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) raw[i] = load_raw<T, V>(st + (long long)i * a.D);
+  raw[K - 1] = load_raw<T, V>(static_cast<const T*>(a.x) + (long long)b * a.x_row + c);
+  float acc[V];
+#pragma unroll
+  for (int q = 0; q < V; ++q) acc[q] = a.bias ? a.bias[c + q] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    float w[V], f[V];
+    load_params<V>(a.w + (long long)j * a.D + c, w);
+    unpack<T, V>(raw[K - 1 - j], f);
+#pragma unroll
+    for (int q = 0; q < V; ++q) acc[q] = fmaf(w[q], f[q], acc[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < V; ++q) acc[q] = a.act ? acc[q] * fast_sigmoid(acc[q]) : acc[q];
+  store_vec<T, V>(static_cast<T*>(a.y) + (long long)b * a.D + c, acc);
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i)
+    *reinterpret_cast<typename Pack<T, V>::U*>(st + (long long)i * a.D) = raw[i + 1];
+}
+
+// With g[t] = dy[t] act'(pre[t]):  dx[t] = sum_j w[j] g[t + j],  dw[j] = sum_t g[t] x[t - j],
+// dbias = sum_t g[t]; row i of dstate_out adds to dx of history row n + i. A thread walks its
+// run and the width - 1 tokens behind it (their g enters its last dx), and adds dw and dbias
+// of its own tokens into one row of partials, which column_sums joins in a fixed order.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int cblocks, int run) {
+  const int c = ((blockIdx.x % cblocks) * kConvThreads + threadIdx.x) * V;
+  if (c >= a.D) return;
+  const int b = blockIdx.y;
+  const int r = blockIdx.x / cblocks, runs = gridDim.x / cblocks;
+  const int t0 = r * run, t1 = min(a.N, t0 + run);
+  const int n = sequence_length(a.lens, b, a.N);
+  const T* x = static_cast<const T*>(a.x) + (long long)b * a.N * a.x_row + c;
+  const T* dy = static_cast<const T*>(a.dy) + (long long)b * a.N * a.D + c;
+  T* dx = static_cast<T*>(a.dx) + (long long)b * a.N * a.D + c;
+  float w[K][V], bias[V], dw[K][V], db[V];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    load_params<V>(a.w + (long long)j * a.D + c, w[j]);
+#pragma unroll
+    for (int q = 0; q < V; ++q) dw[j][q] = 0.0f;
+  }
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+    bias[q] = a.bias ? a.bias[c + q] : 0.0f;
+    db[q] = 0.0f;
+  }
+  float win[K - 1][V], g[K][V];   // win[j - 1] = x[s - j], g[j] = g[s - j]
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+#pragma unroll
+    for (int q = 0; q < V; ++q) g[j][q] = 0.0f;
+  if (t0 < n) {
+#pragma unroll
+    for (int j = 1; j < K; ++j) history_row<T, V, K>(a, b, c, (long long)t0 - j + K - 1, win[j - 1]);
+  } else {
+#pragma unroll
+    for (int j = 1; j < K; ++j)
+#pragma unroll
+      for (int q = 0; q < V; ++q) win[j - 1][q] = 0.0f;
+  }
+  const int s1 = t1 + K - 1;
+  for (int s0 = t0; s0 < s1; s0 += kAhead) {
+    typename Pack<T, V>::U rx[kAhead], rg[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (s0 + i < min(s1, n)) {
+        rx[i] = load_raw<T, V>(x + (long long)(s0 + i) * a.x_row);
+        rg[i] = load_raw<T, V>(dy + (long long)(s0 + i) * a.D);
+      }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int s = s0 + i;
+      if (s >= s1) break;
+      float cur[V];
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+#pragma unroll
+        for (int j = K - 1; j > 0; --j) g[j][q] = g[j - 1][q];
+        g[0][q] = 0.0f;
+        cur[q] = 0.0f;
+      }
+      if (s < n) {
+        unpack<T, V>(rx[i], cur);
+        unpack<T, V>(rg[i], g[0]);
+        if (a.act) {
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            float pre = fmaf(w[0][q], cur[q], bias[q]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) pre = fmaf(w[j][q], win[j - 1][q], pre);
+            const float sg = fast_sigmoid(pre);
+            g[0][q] *= sg * fmaf(pre, 1.0f - sg, 1.0f);
+          }
+        }
+        if (s < t1) {
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            dw[0][q] = fmaf(g[0][q], cur[q], dw[0][q]);
+#pragma unroll
+            for (int j = 1; j < K; ++j) dw[j][q] = fmaf(g[0][q], win[j - 1][q], dw[j][q]);
+            db[q] += g[0][q];
+          }
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+#pragma unroll
+        for (int j = K - 2; j > 0; --j) win[j][q] = win[j - 1][q];
+        win[0][q] = cur[q];
+      }
+      const int t = s - (K - 1);   // the row of dx that g[s] completes
+      if (t >= t0 || r == 0) {
+        float o[V];
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          o[q] = w[0][q] * g[K - 1][q];
+#pragma unroll
+          for (int j = 1; j < K; ++j) o[q] = fmaf(w[j][q], g[K - 1 - j][q], o[q]);
+        }
+        const int i_out = t + K - 1 - n;   // the row of dstate_out that this row became
+        if (a.dstate_out && i_out >= 0 && i_out < K - 1) {
+          float f[V];
+          load_vec<T, V>(static_cast<const T*>(a.dstate_out) +
+                             ((long long)b * (K - 1) + i_out) * a.D + c, f);
+#pragma unroll
+          for (int q = 0; q < V; ++q) o[q] += f[q];
+        }
+        if (t >= 0)
+          store_vec<T, V>(dx + (long long)t * a.D, o);
+        else if (a.dstate_in)
+          store_vec<T, V>(static_cast<T*>(a.dstate_in) +
+                              ((long long)b * (K - 1) + t + K - 1) * a.D + c, o);
+      }
+    }
+  }
+  float* part = a.partials + ((long long)b * runs + r) * (K + 1) * a.D + c;
+#pragma unroll
+  for (int q = 0; q < V; ++q) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) part[(long long)j * a.D + q] = dw[j][q];
+    part[(long long)K * a.D + q] = db[q];
+  }
+}
+
+// 32 columns x 8 row groups per block; row group g adds rows g, g + 8, ... in order.
+__global__ void __launch_bounds__(256) column_sums_kernel(const float* part, long long R, long long C,
+                                                          float* out0, long long n0, float* out1) {
+  __shared__ float acc[8][33];
+  const long long c = (long long)blockIdx.x * 32 + threadIdx.x;
+  float v = 0.0f;
+  if (c < C) {
+#pragma unroll 4
+    for (long long r = threadIdx.y; r < R; r += 8) v += part[r * C + c];
+  }
+  acc[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < C) {
+#pragma unroll
+    for (int g = 1; g < 8; ++g) v += acc[g][threadIdx.x];
+    if (c < n0) {
+      if (out0) out0[c] = v;
+    } else if (out1) {
+      out1[c - n0] = v;
+    }
+  }
+}
+
+// Tokens of one thread's run. Long runs re-read less halo (width - 1 rows per run); short
+// ones give small problems enough threads: at least some 1000 per SM while the run is over 8.
+int conv_run(int B, int N, int D, int V) {
+  const long long groups = (long long)B * ((D + V - 1) / V);
+  int run = 64;
+  while (run > 8 && groups * ((N + run - 1) / run) < 148LL * 1024) run /= 2;
+  return run;
+}
+
+enum Pass { FWD, BWD, STEP };
+
+// Channels of a vector thread: 16 bytes, 4 elements where a thread holds more rows in
+// registers than that leaves room for (the backward's 4 * width + 2, wide forward windows).
+constexpr int kBwdVec = 4;
+template <typename T>
+constexpr int conv_vec(Pass pass, int width) {
+  return pass == BWD || (pass == FWD && width > 5) ? 4 : 16 / (int)sizeof(T);
+}
+
+template <typename T, Pass P, int V, int K>
+cudaError_t launch_width(const ConvArgs& a, cudaStream_t s) {
+  const int cblocks = ((a.D + V - 1) / V + kConvThreads - 1) / kConvThreads;
+  if constexpr (P == STEP) {
+    conv_step_kernel<T, V, K><<<dim3(cblocks, a.B), kConvThreads, 0, s>>>(a);
+  } else {
+    const int run = conv_run(a.B, a.N, a.D, P == BWD ? kBwdVec : V);
+    const int runs = a.N > 0 ? (a.N + run - 1) / run : 1;
+    const dim3 grid((unsigned)((long long)cblocks * runs), a.B);
+    if constexpr (P == FWD)
+      conv_fwd_kernel<T, V, K><<<grid, kConvThreads, 0, s>>>(a, cblocks, run);
+    else
+      conv_bwd_kernel<T, V, K><<<grid, kConvThreads, 0, s>>>(a, cblocks, run);
+  }
+  return cudaGetLastError();
+}
+
+// Vector accesses when the channels, the row stride and every buffer allow them, else one
+// element at a time.
+template <typename T, Pass P, int K>
+cudaError_t launch_vec(const ConvArgs& a, cudaStream_t s) {
+  constexpr int V = conv_vec<T>(P, K);
+  bool vec = a.D % V == 0 && a.x_row % V == 0;
+  for (const void* p : {a.x, a.state_in, (const void*)a.y, (const void*)a.state_out, a.dy,
+                        a.dstate_out, (const void*)a.dx, (const void*)a.dstate_in})
+    vec = vec && reinterpret_cast<uintptr_t>(p) % (V * sizeof(T)) == 0;
+  return vec ? launch_width<T, P, V, K>(a, s) : launch_width<T, P, 1, K>(a, s);
+}
+
+template <typename T, Pass P>
+cudaError_t launch_typed(const ConvArgs& a, cudaStream_t s) {
+  switch (a.width) {
+    case 2: return launch_vec<T, P, 2>(a, s);
+    case 3: return launch_vec<T, P, 3>(a, s);
+    case 4: return launch_vec<T, P, 4>(a, s);
+    case 5: return launch_vec<T, P, 5>(a, s);
+    case 6: return launch_vec<T, P, 6>(a, s);
+    case 7: return launch_vec<T, P, 7>(a, s);
+    case 8: return launch_vec<T, P, 8>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <Pass P>
+cudaError_t launch(int dt, const ConvArgs& a, cudaStream_t s) {
+  return dt == DT_BF16 ? launch_typed<bf16, P>(a, s) : launch_typed<float, P>(a, s);
+}
+
+}  // namespace
+
+cudaError_t column_sums(const float* part, long long R, long long C, float* out0, long long n0,
+                        float* out1, cudaStream_t s) {
+  column_sums_kernel<<<(unsigned)((C + 31) / 32), dim3(32, 8), 0, s>>>(part, R, C, out0, n0, out1);
+  return cudaGetLastError();
+}
+
+cudaError_t conv_fwd(int dt, const ConvArgs& a, cudaStream_t s) { return launch<FWD>(dt, a, s); }
+cudaError_t conv_step(int dt, const ConvArgs& a, cudaStream_t s) { return launch<STEP>(dt, a, s); }
+cudaError_t conv_bwd(int dt, const ConvArgs& a, cudaStream_t s) { return launch<BWD>(dt, a, s); }
+
+long long conv_bwd_rows(int B, int N, int D) {
+  const int run = conv_run(B, N, D, kBwdVec);
+  return (long long)B * (N > 0 ? (N + run - 1) / run : 1);
+}
+
+}  // namespace ttt

@@ -4,6 +4,10 @@ workspace with torch, and calls the library. No arithmetic of the layer happens 
 Shapes (see include/ttt.h): q, k, v [B,H,N,h] (bf16 or fp32, contiguous, on the GPU);
 eta [B,H,N] fp32; W0, W2 [H,h,m] fp32 ([H,m,h] with w_in_layout=1); W1 [H,m,h] fp32
 ([H,h,m] with w1_layout=1).
+
+The token-mixer operators (short_conv_*, head_norm_rope_*, selective_scan_*) take token-major
+inputs [B,N,...] that may be slices of a wider projection (one stride between all tokens);
+they run on the device of their first tensor, on its current stream unless ``stream`` is given.
 """
 from __future__ import annotations
 
@@ -245,3 +249,306 @@ def lm_target(X0, conv_w, W_target, *, out=None, ws=None, stream=None):
         ws = workspace(abi.ttt_lm_target_workspace_bytes(N, d), X0.device)
     abi.ttt_lm_target(N, d, X0, conv_w, W_target, out, ws, stream=stream)
     return out
+
+
+# ----------------------------------------------------------------- the token mixer's operators
+ACTS = {None: abi.TTT_ACT_NONE, "silu": abi.TTT_ACT_SILU}
+NORMS = {None: abi.TTT_NORM_NONE, "rms": abi.TTT_NORM_RMS, "l2": abi.TTT_NORM_L2}
+PAIRS = {"halves": abi.TTT_PAIRS_HALVES, "interleaved": abi.TTT_PAIRS_INTERLEAVED}
+
+
+class _On:
+    """The device of a call's tensors as the current one (a no-op when it already is)."""
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _choice(table, key, name):
+    if key not in table:
+        raise ValueError(f"{name} must be one of {list(table)}, got {key!r}")
+    return table[key]
+
+
+def _dense(t, name, shape, dtype, device):
+    """A contiguous tensor of exactly this shape and type, or None."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name, lead, width, dtype, device):
+    """Elements between the tokens of ``t`` [*lead, *width] (lead: B, N or B); 0 when None."""
+    if t is None:
+        return 0
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != lead + width:
+        raise ValueError(f"{name} must be {lead + width}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.is_contiguous():
+        return 0
+    n = 1
+    strides = t.stride()
+    for size, st in zip(reversed(width), reversed(strides[len(lead):])):
+        if size > 1 and st != n:
+            raise ValueError(f"{name}: the elements of a token must be contiguous")
+        n *= size
+    row = tokens = None      # the innermost of the leading sizes above 1 sets the stride
+    for size, st in zip(reversed(lead), reversed(strides[:len(lead)])):
+        if size <= 1:
+            continue
+        if row is None:
+            row, tokens = st, size
+        elif st != row * tokens:
+            raise ValueError(f"{name}: all tokens must be one stride apart")
+    if row is None:
+        return 0
+    if row < n:
+        raise ValueError(f"{name}: tokens overlap (stride {row}, {n} elements)")
+    return row
+
+
+def _first(t, name, dims):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {tuple(t.shape)}")
+    return t.device
+
+
+def _conv_desc(x, w, bias, act, state, lens, lead):
+    device = x.device
+    D = x.shape[-1]
+    if w.dim() != 2:
+        raise ValueError(f"w must be [width, {D}], got {tuple(w.shape)}")
+    width = w.shape[0]
+    _dense(w, "w", (width, D), torch.float32, device)
+    _dense(bias, "bias", (D,), torch.float32, device)
+    _dense(state, "state", (lead[0], width - 1, D), x.dtype, device)
+    _dense(lens, "lens", (lead[0],), torch.int32, device)
+    return abi.ttt_conv_desc(lead[0], lead[1] if len(lead) > 1 else 1, D, width, _dtype_code(x),
+                             _choice(ACTS, act, "act"), _rows(x, "x", lead, (D,), x.dtype, device))
+
+
+def short_conv_fwd(x, w, *, bias=None, act="silu", state=None, lens=None, return_state=True,
+                   out=None, state_out=None, stream=None):
+    """Short causal depthwise convolution of x [B,N,D] with taps w [width,D] (tap j multiplies
+    x[t-j]), after the inputs in ``state`` [B,width-1,D] (zeros when None). ``act`` is "silu" or
+    None; ``lens`` [B] int32 gives the tokens of padded sequences. Returns (y, the state after
+    the last token or None). ``state_out`` may be ``state``."""
+    device = _first(x, "x", 3)
+    desc = _conv_desc(x, w, bias, act, state, lens, tuple(x.shape[:2]))
+    B, N, D = x.shape
+    shape = (B, desc.width - 1, D)
+    with _On(device):
+        if out is None:
+            out = torch.empty((B, N, D), dtype=x.dtype, device=device)
+        _dense(out, "out", (B, N, D), x.dtype, device)
+        if state_out is None and return_state:
+            state_out = torch.empty(shape, dtype=x.dtype, device=device)
+        _dense(state_out, "state_out", shape, x.dtype, device)
+        abi.ttt_short_conv_fwd(desc, x, w, bias, state, lens, out, state_out, stream=stream)
+    return out, state_out
+
+
+def short_conv_step(x, w, state, *, bias=None, act="silu", out=None, stream=None):
+    """The next token x [B,D] of B sequences; ``state`` [B,width-1,D] is shifted in place.
+    Returns y [B,D]."""
+    device = _first(x, "x", 2)
+    desc = _conv_desc(x, w, bias, act, state, None, (x.shape[0],))
+    with _On(device):
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        _dense(out, "out", x.shape, x.dtype, device)
+        abi.ttt_short_conv_step(desc, x, w, bias, state, out, stream=stream)
+    return out
+
+
+def short_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lens=None, dstate=None,
+                   ws=None, stream=None):
+    """Backward of short_conv_fwd for dy [B,N,D] and ``dstate``, the gradient of the returned
+    state (or None). Returns dx, dw, dbias (None without bias), the gradient of ``state`` (None
+    without it)."""
+    device = _first(x, "x", 3)
+    desc = _conv_desc(x, w, bias, act, state, lens, tuple(x.shape[:2]))
+    B, N, D = x.shape
+    _dense(dy, "dy", (B, N, D), x.dtype, device)
+    _dense(dstate, "dstate", (B, desc.width - 1, D), x.dtype, device)
+    with _On(device):
+        dx = torch.empty((B, N, D), dtype=x.dtype, device=device)
+        dw = torch.empty_like(w)
+        dbias = None if bias is None else torch.empty_like(bias)
+        dstate_in = None if state is None else torch.empty_like(state)
+        if ws is None:
+            ws = workspace(abi.ttt_short_conv_bwd_workspace_bytes(desc), device)
+        abi.ttt_short_conv_bwd(desc, x, w, bias, state, lens, dy, dstate, dx, dw, dbias, dstate_in,
+                               ws, stream=stream)
+    return dx, dw, dbias, dstate_in
+
+
+def _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs):
+    some = next((t for t in (q, k, v) if t is not None), None)
+    if some is None:
+        raise ValueError("one of q, k and v must be given")
+    device = _first(some, "q, k and v", 4)
+    B, N, _, h = some.shape
+    row, H = [], []
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if t is not None and t.dim() != 4:
+            raise ValueError(f"{name} must be [B, N, heads, h], got {tuple(t.shape)}")
+        n = 0 if t is None else t.shape[2]
+        H.append(n)
+        row.append(_rows(t, name, (B, N), (n, h), some.dtype, device))
+    _dense(wq, "wq", (h,), torch.float32, device)
+    _dense(wk, "wk", (h,), torch.float32, device)
+    _dense(positions, "positions", (B, N), torch.int32, device)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _dense(inv_freq, "inv_freq", (rot // 2,), torch.float32, device)
+    return abi.ttt_heads_desc(B, N, H[0], H[1], H[2], h, _dtype_code(some),
+                              _choice(NORMS, norm, "norm"), rot, _choice(PAIRS, pairs, "pairs"),
+                              eps, pos0, row[0], row[1], row[2]), some
+
+
+def head_norm_rope_fwd(q, k, v=None, *, wq=None, wk=None, norm="l2", eps=1e-6, inv_freq=None,
+                       positions=None, pos0=0, pairs="halves", stream=None):
+    """The layer's q, k, v [B,H,N,h] from the projection's token-major q, k, v [B,N,H,h] (any
+    of them None): every query and key head normed ("l2", "rms" or None) and scaled by wq / wk
+    [h], its first 2 * len(inv_freq) elements rotated by position * inv_freq (positions [B,N]
+    int32, or pos0 + t), and v laid out. Returns (q, k, v)."""
+    desc, some = _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs)
+    B, N, _, h = some.shape
+    with _On(some.device):
+        out = [None if t is None else
+               torch.empty((B, t.shape[2], N, h), dtype=t.dtype, device=some.device)
+               for t in (q, k, v)]
+        abi.ttt_head_norm_rope_fwd(desc, q, k, v, wq, wk, inv_freq, positions, *out, stream=stream)
+    return tuple(out)
+
+
+def head_norm_rope_bwd(q, k, v, dq, dk, dv, *, wq=None, wk=None, norm="l2", eps=1e-6,
+                       inv_freq=None, positions=None, pos0=0, pairs="halves", ws=None,
+                       stream=None):
+    """Backward of head_norm_rope_fwd for the gradients dq, dk, dv [B,H,N,h] of its outputs.
+    Returns the gradients of q, k, v [B,N,H,h] and of wq, wk (None for what was None)."""
+    desc, some = _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs)
+    B, N, _, h = some.shape
+    device = some.device
+    for t, g, name in ((q, dq, "dq"), (k, dk, "dk"), (v, dv, "dv")):
+        if (t is None) != (g is None):
+            raise ValueError(f"{name} must be given exactly when its tensor is")
+        if g is not None:
+            _dense(g, name, (B, t.shape[2], N, h), some.dtype, device)
+    with _On(device):
+        out = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
+               for t in (q, k, v)]
+        dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+        if ws is None and (wq is not None or wk is not None):
+            ws = workspace(abi.ttt_head_norm_rope_bwd_workspace_bytes(desc), device)
+        abi.ttt_head_norm_rope_bwd(desc, q, k, wq, wk, inv_freq, positions, dq, dk, dv, *out, dwq,
+                                   dwk, ws, stream=stream)
+    return (*out, dwq, dwk)
+
+
+def _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, lens, lead):
+    device, dtype = u.device, u.dtype
+    d = u.shape[-1]
+    if A.dim() != 2:
+        raise ValueError(f"A must be [{d}, S], got {tuple(A.shape)}")
+    if Bm.dim() != len(lead) + 2:
+        raise ValueError(f"Bm must be {lead} + (G, S), got {tuple(Bm.shape)}")
+    S, G = A.shape[1], Bm.shape[-2]
+    f32 = torch.float32
+    _dense(A, "A", (d, S), f32, device)
+    _dense(D, "D", (d,), f32, device)
+    _dense(dt_bias, "dt_bias", (d,), f32, device)
+    _dense(state, "state", (lead[0], d, S), f32, device)
+    _dense(lens, "lens", (lead[0],), torch.int32, device)
+    return abi.ttt_scan_desc(lead[0], lead[1] if len(lead) > 1 else 1, d, S, G, _dtype_code(u),
+                             int(bool(softplus)), 0, _rows(u, "u", lead, (d,), dtype, device),
+                             _rows(dt, "dt", lead, (d,), dtype, device),
+                             _rows(z, "z", lead, (d,), dtype, device),
+                             _rows(Bm, "Bm", lead, (G, S), dtype, device),
+                             _rows(Cm, "Cm", lead, (G, S), dtype, device))
+
+
+def selective_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus=True,
+                       state=None, lens=None, return_state=True, out=None, state_out=None, ws=None,
+                       stream=None):
+    """Selective state space scan of u, dt [B,N,D] with A [D,S], Bm, Cm [B,N,G,S], the skip D
+    [D], the gate z [B,N,D] and dt_bias [D], from ``state`` [B,D,S] fp32 (zeros when None);
+    ``lens`` [B] int32 gives the tokens of padded sequences. Returns (y [B,N,D], the state after
+    the last token or None). ``state_out`` may be ``state``."""
+    device = _first(u, "u", 3)
+    desc = _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, lens, tuple(u.shape[:2]))
+    shape = (desc.B, desc.D, desc.S)
+    with _On(device):
+        if out is None:
+            out = torch.empty(u.shape, dtype=u.dtype, device=device)
+        _dense(out, "out", u.shape, u.dtype, device)
+        if state_out is None and return_state:
+            state_out = torch.empty(shape, dtype=torch.float32, device=device)
+        _dense(state_out, "state_out", shape, torch.float32, device)
+        if ws is None:
+            need = abi.ttt_selective_scan_workspace_bytes(desc, 0)
+            ws = workspace(need, device) if need else None
+        abi.ttt_selective_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, out,
+                                   state_out, ws, stream=stream)
+    return out, state_out
+
+
+def selective_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, softplus=True,
+                        out=None, stream=None):
+    """The next token of B sequences: u, dt, z [B,D], Bm, Cm [B,G,S]; ``state`` [B,D,S] fp32 is
+    updated in place. Returns y [B,D]."""
+    device = _first(u, "u", 2)
+    desc = _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, None, (u.shape[0],))
+    with _On(device):
+        if out is None:
+            out = torch.empty(u.shape, dtype=u.dtype, device=device)
+        _dense(out, "out", u.shape, u.dtype, device)
+        abi.ttt_selective_scan_step(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, out,
+                                    stream=stream)
+    return out
+
+
+def selective_scan_bwd(u, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=None, softplus=True,
+                       state=None, lens=None, dstate=None, ws=None, stream=None):
+    """Backward of selective_scan_fwd for dy [B,N,D] and ``dstate``, the gradient of the
+    returned state (or None). Returns du, ddt, dA, dBm, dCm, dD, dz, ddt_bias, dstate_in (None
+    for what was None)."""
+    device = _first(u, "u", 3)
+    desc = _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, lens, tuple(u.shape[:2]))
+    _dense(dy, "dy", u.shape, u.dtype, device)
+    _dense(dstate, "dstate", (desc.B, desc.D, desc.S), torch.float32, device)
+
+    def new(t):
+        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
+
+    with _On(device):
+        du, ddt, dA, dB, dC = new(u), new(dt), new(A), new(Bm), new(Cm)
+        dD, dz, dbias, dstate_in = new(D), new(z), new(dt_bias), new(state)
+        if ws is None:
+            ws = workspace(abi.ttt_selective_scan_workspace_bytes(desc, 1), device)
+        abi.ttt_selective_scan_bwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, dy, dstate,
+                                   du, ddt, dA, dB, dC, dD, dz, dbias, dstate_in, ws,
+                                   stream=stream)
+    return du, ddt, dA, dB, dC, dD, dz, dbias, dstate_in
