@@ -24,6 +24,37 @@ __device__ __forceinline__ typename Pack<T, V>::U load_raw(const T* p) {
   return *reinterpret_cast<const typename Pack<T, V>::U*>(p);
 }
 
+// The same load where it stands, or zero when `on` is false: the compiler may sink a plain load
+// behind the arithmetic it is meant to run under, down to the first use of its value, and a
+// load in a branch is waited for where the branch ends.
+__device__ __forceinline__ void load_here(const void* p, bool on, unsigned short& u) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %2, 0;\nmov.u16 %0, 0;\n@q ld.global.u16 %0, [%1];\n}"
+               : "=h"(u) : "l"(p), "r"((unsigned)on));
+}
+__device__ __forceinline__ void load_here(const void* p, bool on, unsigned& u) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %2, 0;\nmov.u32 %0, 0;\n@q ld.global.u32 %0, [%1];\n}"
+               : "=r"(u) : "l"(p), "r"((unsigned)on));
+}
+__device__ __forceinline__ void load_here(const void* p, bool on, uint2& u) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %3, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\n"
+               "@q ld.global.v2.u32 {%0, %1}, [%2];\n}"
+               : "=r"(u.x), "=r"(u.y) : "l"(p), "r"((unsigned)on));
+}
+__device__ __forceinline__ void load_here(const void* p, bool on, uint4& u) {
+  asm volatile("{\n.reg .pred q;\nsetp.ne.u32 q, %5, 0;\nmov.u32 %0, 0;\nmov.u32 %1, 0;\n"
+               "mov.u32 %2, 0;\nmov.u32 %3, 0;\n@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n}"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p), "r"((unsigned)on));
+}
+
+// Asynchronous copy of BYTES (4, 8 or 16) bytes to shared memory, or zeros when `on` is false.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                   (unsigned)__cvta_generic_to_shared(dst)), "l"(src), "n"(BYTES), "r"(on ? BYTES : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const typename Pack<T, V>::U& u, float (&f)[V]) {
   union { typename Pack<T, V>::U u; T t[V]; } x;
@@ -50,16 +81,32 @@ __device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
 
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
-  union { typename Pack<T, V>::U u; T t[V]; } x;
+  if constexpr (V * sizeof(T) > 16) {
+    float lo[V / 2], hi[V / 2];
 #pragma unroll
-  for (int i = 0; i < V; ++i) x.t[i] = from_f32<T>(f[i]);
-  *reinterpret_cast<typename Pack<T, V>::U*>(p) = x.u;
+    for (int i = 0; i < V / 2; ++i) {
+      lo[i] = f[i];
+      hi[i] = f[V / 2 + i];
+    }
+    store_vec<T, V / 2>(p, lo);
+    store_vec<T, V / 2>(p + V / 2, hi);
+    return;
+  } else {
+    union { typename Pack<T, V>::U u; T t[V]; } x;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x.t[i] = from_f32<T>(f[i]);
+    *reinterpret_cast<typename Pack<T, V>::U*>(p) = x.u;
+  }
 }
 
-// sigmoid with the hardware exponential and division (relative error some 1e-7 (1 + |a|)):
-// the accurate forms cost more instructions than the memory-bound kernels here have to spare.
+// sigmoid with the hardware exponential and reciprocal (relative error some 1e-7 (1 + |a|)): the
+// accurate forms cost more instructions than these kernels have to spare. exp(-a) past fp32's
+// range gives 1 / inf = 0.
 __device__ __forceinline__ float fast_sigmoid(float a) {
-  return __fdividef(1.0f, 1.0f + __expf(-a));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return r;
 }
 
 }  // namespace ttt

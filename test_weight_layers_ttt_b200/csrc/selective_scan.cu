@@ -16,6 +16,8 @@
 // pass takes each chunk's end state from zero (its decay is exp(A sum delta), one number per
 // state), scan_join carries the states over the chunks, and the outputs pass starts every chunk
 // from its state. That doubles the exponentials, so it is done only for few channels.
+#include <algorithm>
+
 #include "mixer.h"
 #include "mixer_common.cuh"
 
@@ -63,54 +65,51 @@ __device__ __forceinline__ f2 ex2_2(f2 v) {
   return pack2(ex2(lo), ex2(hi));
 }
 
-// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1]. log1p(e) / e is a polynomial of
-// degree 9, interpolated at the Chebyshev nodes of [0, 1] (relative error 1.2e-7 in fp32): it
-// keeps the relative accuracy of small steps, which a logarithm of 1 + e loses, without a
-// second special-function result.
+// softplus(x) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], for two values. log1p(e) / e is
+// a polynomial of degree 9, interpolated at the Chebyshev nodes of [0, 1] (relative error 1.2e-7
+// in fp32): it keeps the relative accuracy of small steps, which a logarithm of 1 + e loses, and
+// leaves the exponential unit alone.
+__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ f2 softplus2(f2 x) {
+  float lo, hi;
+  unpack2(x, lo, hi);
+  const f2 e = ex2_2(pack2(-fabsf(lo) * kLog2e, -fabsf(hi) * kLog2e));
+  f2 p = both(-0.0031760570127516985f);
+  p = fma2(p, e, both(0.019542526453733444f));
+  p = fma2(p, e, both(-0.056373611092567444f));
+  p = fma2(p, e, both(0.10543623566627502f));
+  p = fma2(p, e, both(-0.1526966691017151f));
+  p = fma2(p, e, both(0.1966327428817749f));
+  p = fma2(p, e, both(-0.24951615929603577f));
+  p = fma2(p, e, both(0.33329710364341736f));
+  p = fma2(p, e, both(-0.49999892711639404f));
+  p = fma2(p, e, both(1.0f));
+  return fma2(e, p, pack2(fmaxf(lo, 0.0f), fmaxf(hi, 0.0f)));
+}
 __device__ __forceinline__ float softplus(float x) {
-  const float e = ex2(-fabsf(x) * kLog2e);
-  float p = -0.0031760570127516985f;
-  p = fmaf(p, e, 0.019542526453733444f);
-  p = fmaf(p, e, -0.056373611092567444f);
-  p = fmaf(p, e, 0.10543623566627502f);
-  p = fmaf(p, e, -0.1526966691017151f);
-  p = fmaf(p, e, 0.1966327428817749f);
-  p = fmaf(p, e, -0.24951615929603577f);
-  p = fmaf(p, e, 0.33329710364341736f);
-  p = fmaf(p, e, -0.49999892711639404f);
-  p = fmaf(p, e, 1.0f);
-  return fmaxf(x, 0.0f) + e * p;
+  float lo, hi;
+  unpack2(softplus2(pack2(x, 0.0f)), lo, hi);
+  return lo;
 }
 
 // ---------------------------------------------------------------- tiles
-// SL lanes share a channel: lane = channel pair * SL + state group, 4 states per lane.
-template <int SL> struct Tile {
-  static constexpr int SP = 4 * SL;                        // padded states
-  static constexpr int CL = 32 / SL;                       // channel pairs of a warp
-  static constexpr int WC = 2 * CL;                        // channels of a warp
-  static constexpr int CB = kWarps * WC;                   // channels of a block
-  static constexpr int TT = SL == 16 ? 32 : 4 * SL;        // tokens of a staged tile
-  static constexpr int EPT = TT * CB / kThreads;           // channels a thread stages (one token)
-  static constexpr int TPR = CB / EPT;                     // threads of a token's row
-};
-
 // N consecutive elements of a row; VEC: in accesses of up to 16 bytes (all N or none valid).
 template <typename T, int N, bool VEC> struct Raw {
   static constexpr int W = N * sizeof(T) > 16 ? 16 / (int)sizeof(T) : N;
   union {
     T t[N];
     typename Pack<T, W>::U u[N / W];
+    typename Pack<T, 1>::U e[N];
   };
   __device__ __forceinline__ void load(const T* p, int valid) {
     if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < N / W; ++i) {
-        if (valid > 0) u[i] = load_raw<T, W>(p + i * W);
-        else u[i] = typename Pack<T, W>::U{};
+        load_here(p + i * W, valid > 0, u[i]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) t[i] = i < valid ? p[i] : from_f32<T>(0.0f);
+      for (int i = 0; i < N; ++i) load_here(p + i, i < valid, e[i]);
     }
   }
   __device__ __forceinline__ void store(T* p, int valid) const {
@@ -145,65 +144,6 @@ __device__ __forceinline__ int sequence_length(const int* lens, int b, int N) {
   return lens ? min(max(lens[b], 0), N) : N;
 }
 
-// A lane's 4 states of its 2 channels, scaled; zero outside the channels and states.
-template <int SL>
-__device__ __forceinline__ void load_A(const ScanArgs& a, int c, int c1, int s0, f2 (&A2)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool on = s0 + i < a.S;
-    const float lo = on && c < c1 ? a.A[(long long)c * a.S + s0 + i] : 0.0f;
-    const float hi = on && c + 1 < c1 ? a.A[(long long)(c + 1) * a.S + s0 + i] : 0.0f;
-    A2[i] = pack2(lo * kLog2e, hi * kLog2e);
-  }
-}
-
-// Element s of the lane's channel pair in a [D, S] array.
-__device__ __forceinline__ f2 load_pair(const float* p, int c, int c1, int s, int S) {
-  const float lo = c < c1 && s < S ? p[(long long)c * S + s] : 0.0f;
-  const float hi = c + 1 < c1 && s < S ? p[(long long)(c + 1) * S + s] : 0.0f;
-  return pack2(lo, hi);
-}
-__device__ __forceinline__ void store_pair(float* p, int c, int c1, int s, int S, f2 v) {
-  float lo, hi;
-  unpack2(v, lo, hi);
-  if (s < S) {
-    if (c < c1) p[(long long)c * S + s] = lo;
-    if (c + 1 < c1) p[(long long)(c + 1) * S + s] = hi;
-  }
-}
-
-// The lane's 4 states of both channels in a [D, SP] array of the workspace (16-byte rows).
-template <int SL>
-__device__ __forceinline__ void load_tile(const float* p, int c, int c1, int s0, f2 (&v)[4]) {
-  float lo[4] = {}, hi[4] = {};
-  if (c < c1) load_vec<float, 4>(p + (long long)c * 4 * SL + s0, lo);
-  if (c + 1 < c1) load_vec<float, 4>(p + (long long)(c + 1) * 4 * SL + s0, hi);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = pack2(lo[i], hi[i]);
-}
-template <int SL>
-__device__ __forceinline__ void store_tile(float* p, int c, int c1, int s0, const f2 (&v)[4]) {
-  float lo[4], hi[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) unpack2(v[i], lo[i], hi[i]);
-  if (c < c1) store_vec<float, 4>(p + (long long)c * 4 * SL + s0, lo);
-  if (c + 1 < c1) store_vec<float, 4>(p + (long long)(c + 1) * 4 * SL + s0, hi);
-}
-
-// TOKENS rows of B or C for one group from token t on, each value twice (both channels of a
-// pair multiply by it), zero behind `live` tokens and S states.
-template <typename T, int SL, int TOKENS>
-__device__ __forceinline__ void stage_bc(f2* dst, const void* src, long long row, const ScanArgs& a,
-                                         int b, int g, int t, int live) {
-  constexpr int SP = 4 * SL;
-  const T* p = static_cast<const T*>(src) + ((long long)b * a.N + t) * row + (long long)g * a.S;
-  for (int i = threadIdx.x; i < TOKENS * SP; i += kThreads) {
-    const int k = i / SP, s = i % SP;
-    const float v = k < live && s < a.S ? to_f32(p[k * row + s]) : 0.0f;
-    dst[i] = pack2(v, v);
-  }
-}
-
 // Sums `n` values of each lane over the LANES lanes that differ in the lane bits
 // [SHIFT, SHIFT + log2 LANES): afterwards v[0 .. max(1, n / LANES)) of a lane are the sums
 // whose index starts with that lane's bits (lanes share a sum where n < LANES).
@@ -227,93 +167,154 @@ __device__ __forceinline__ void butterfly(float (&v)[NV], int lane) {
 }
 
 // ---------------------------------------------------------------- forward
+// A lane holds M states of one channel, packed in pairs; SL lanes share a channel (lane =
+// state group * CH + channel: groups in the high lane bits, so that a 16-byte read of B or C,
+// the same for all channels, takes 2 cycles of the shared memory pipe instead of 4).
+constexpr int kFwdWarps = 4, kFwdThreads = 32 * kFwdWarps;
+
+template <int SL> struct FwdTile {
+  static constexpr int M = 4;
+  static constexpr int SP = M * SL;                        // padded states
+  static constexpr int CH = 32 / SL;                       // channels of a warp
+  static constexpr int CB = kFwdWarps * CH;                // channels of a block
+  static constexpr int TT = SL == 2 ? 8 : SL == 4 ? 16 : 32;   // tokens of a staged tile
+  static constexpr int EPT = TT * CB / kFwdThreads;        // channels a thread stages (one token)
+  static constexpr int TPR = CB / EPT;                     // threads of a token's row
+  static constexpr int BCN = TT * SP / 4 / kFwdThreads > 0 ? TT * SP / 4 / kFwdThreads : 1;
+};
+
+// TT rows of B or C of one group, four states at a time: held in registers between the load
+// and the store so that the next tile's loads run under this one's arithmetic.
+template <typename T, int SL>
+struct RowsBC {
+  using L = FwdTile<SL>;
+  Raw<T, 4, true> v[L::BCN];
+  __device__ __forceinline__ void load(const T* p, long long row, int S, bool vec, int live) {
+#pragma unroll
+    for (int j = 0; j < L::BCN; ++j) {
+      const int i = threadIdx.x + j * kFwdThreads, k = i / (L::SP / 4), s = i % (L::SP / 4) * 4;
+      const int on = k < min(live, L::TT) ? S - s : 0;
+      if (vec) {
+        v[j].load(p + k * row + s, on);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) load_here(p + k * row + s + q, q < on, v[j].e[q]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* dst) const {
+#pragma unroll
+    for (int j = 0; j < L::BCN; ++j) {
+      const int i = threadIdx.x + j * kFwdThreads;
+      const float f[4] = {v[j].get(0), v[j].get(1), v[j].get(2), v[j].get(3)};
+      if (i < L::TT * L::SP / 4) store_vec<float, 4>(dst + i * 4, f);
+    }
+  }
+};
+
 // One chunk of one sequence for CB channels. OUT: from the chunk's start state, writing y (and
 // the state behind the last chunk); else from zero, writing the end state and the sum of delta.
 // grid (channel blocks, chunks, B).
 template <typename T, int SL, bool VEC, bool OUT>
-__global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs a, int blocks_per_group) {
-  using L = Tile<SL>;
-  constexpr int TT = L::TT, CB = L::CB, SP = L::SP, EPT = L::EPT;
-  __shared__ __align__(16) float sD[TT * CB], sU[TT * CB];   // delta; u, then y
-  __shared__ __align__(16) f2 sB[TT * SP], sC[OUT ? TT * SP : 2];
+__global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanArgs a, int blocks_per_group,
+                                                               bool vec_b, bool vec_c) {
+  using L = FwdTile<SL>;
+  constexpr int TT = L::TT, CB = L::CB, SP = L::SP, EPT = L::EPT, M = L::M;
+  constexpr bool AHEAD = L::BCN <= 2;   // B and C of the next tile are loaded a tile ahead
+  __shared__ __align__(16) float2 sDU[TT * CB];            // delta; delta u
+  __shared__ __align__(16) float sY[OUT ? SL * TT * CB : 4];   // each state group's sum of C h
+  __shared__ __align__(16) float sB[TT * SP], sC[OUT ? TT * SP : 4];
   const Range r = block_channels(blockIdx.x, blocks_per_group, a.D, a.G, CB);
   const int chunk = blockIdx.y, b = blockIdx.z;
   const int len = sequence_length(a.lens, b, a.N);
   const int t0 = chunk * a.chunk, t1 = min(a.N, t0 + a.chunk), te = min(t1, len);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int sl = lane % SL, cw = warp * L::WC + lane / SL * 2;   // state group; channel in block
-  const int c = r.c0 + cw;
+  const int lane = threadIdx.x % 32, sl = lane / L::CH;
+  const int cw = threadIdx.x / 32 * L::CH + lane % L::CH, c = r.c0 + cw;   // channel in block; channel
+  const bool mine = c < r.c1;
   // staging: EPT channels of one token per thread
   const int row = threadIdx.x / L::TPR, col = threadIdx.x % L::TPR * EPT;
   const int sc = r.c0 + col, valid = min(EPT, r.c1 - sc);
   const long long seq = (long long)b * a.N;
-  float bias[EPT];
+  float bias[EPT], skip[EPT];
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) bias[i] = a.dt_bias && i < valid ? a.dt_bias[sc + i] : 0.0f;
-
-  f2 A2[4], h[4], dsum = 0;
-  load_A<SL>(a, c, r.c1, sl * 4, A2);
-  const long long at = ((long long)b * a.chunks + chunk) * a.D * SP;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    h[i] = 0;
-    if (OUT && a.chunks == 1 && a.state_in)
-      h[i] = load_pair(a.state_in + (long long)b * a.D * a.S, c, r.c1, sl * 4 + i, a.S);
+  for (int i = 0; i < EPT; ++i) {
+    bias[i] = a.dt_bias && i < valid ? a.dt_bias[sc + i] : 0.0f;
+    skip[i] = OUT && a.Dskip && i < valid ? a.Dskip[sc + i] : 0.0f;
   }
-  if (OUT && a.chunks > 1) load_tile<SL>(a.ends + at, c, r.c1, sl * 4, h);
-  // D of the channel whose y this lane writes
-  const int cy = c + (sl & 1);
-  float skip[2];
+  f2 A2[M / 2], h[M / 2];
+  float dsum = 0.0f;
+  const long long at = (((long long)b * a.chunks + chunk) * a.D + c) * SP + sl * M;
+  {
+    float v[M], w[M] = {};
+    const long long io = ((long long)b * a.D + c) * a.S;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) skip[i] = a.Dskip && c + i < r.c1 ? a.Dskip[c + i] : 0.0f;
-  const float skip_y = cy == c ? skip[0] : skip[1];
-
+    for (int i = 0; i < M; ++i) {
+      const int s = sl * M + i;
+      const bool on = mine && s < a.S;
+      v[i] = on ? a.A[(long long)c * a.S + s] * kLog2e : 0.0f;
+      if (OUT && a.chunks > 1) w[i] = mine ? a.ends[at + i] : 0.0f;
+      else if (OUT && a.state_in) w[i] = on ? a.state_in[io + s] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) {
+      A2[i] = pack2(v[2 * i], v[2 * i + 1]);
+      h[i] = pack2(w[2 * i], w[2 * i + 1]);
+    }
+  }
   Raw<T, EPT, VEC> ru, rd, rz;
+  RowsBC<T, SL> rb, rc;
+  const T* pB = static_cast<const T*>(a.Bm) + seq * a.b_row + (long long)r.g * a.S;
+  const T* pC = static_cast<const T*>(a.Cm) + seq * a.c_row + (long long)r.g * a.S;
+  auto fetch_bc = [&](int t) {
+    rb.load(pB + t * a.b_row, a.b_row, a.S, vec_b, te - t);
+    if (OUT) rc.load(pC + t * a.c_row, a.c_row, a.S, vec_c, te - t);
+  };
   auto fetch = [&](int t) {
     const int k = t + row, ok = k < te ? valid : 0;
     ru.load(static_cast<const T*>(a.u) + (seq + k) * a.u_row + sc, ok);
     rd.load(static_cast<const T*>(a.dt) + (seq + k) * a.dt_row + sc, ok);
     if (OUT && a.z) rz.load(static_cast<const T*>(a.z) + (seq + k) * a.z_row + sc, ok);
+    if (AHEAD) fetch_bc(t);
   };
-  if (t0 < te) fetch(t0);
+  fetch(t0);
   for (int t = t0; t < te; t += TT) {
     const bool on = t + row < te;
+    if (!AHEAD) fetch_bc(t);
+    rb.store(sB);
+    if (OUT) rc.store(sC);
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const float raw = rd.get(i) + bias[i];
-      sD[row * CB + col + i] = on && i < valid ? (a.softplus ? softplus(raw) : raw) : 0.0f;
-      sU[row * CB + col + i] = ru.get(i);
+    for (int i = 0; i < EPT; i += 2) {   // (columns behind c1 are staged and not used)
+      f2 d = add2(pack2(rd.get(i), rd.get(i + 1)), pack2(bias[i], bias[i + 1]));
+      if (a.softplus) d = softplus2(d);
+      if (!on) d = 0;
+      float d0, d1;
+      unpack2(d, d0, d1);
+      store_vec<float, 4>(&sDU[row * CB + col + i].x, {d0, d0 * ru.get(i), d1, d1 * ru.get(i + 1)});
     }
-    stage_bc<T, SL, TT>(sB, a.Bm, a.b_row, a, b, r.g, t, te - t);
-    if (OUT) stage_bc<T, SL, TT>(sC, a.Cm, a.c_row, a, b, r.g, t, te - t);
     __syncthreads();
-    const Raw<T, EPT, VEC> gate = rz;
-    if (t + TT < te) fetch(t + TT);
+    const Raw<T, EPT, VEC> uu = ru, zz = rz;
+    fetch(t + TT);   // nothing behind te; unconditional, for a branch would wait for its loads
 
-    constexpr int TB = OUT ? SL / 2 : 1;   // tokens whose sums leave together: SL values
 #pragma unroll 1
-    for (int k0 = 0; k0 < TT; k0 += TB) {
-      float v[SL];
+    for (int k0 = 0; k0 < TT; k0 += 4) {
 #pragma unroll
-      for (int j = 0; j < TB; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int k = k0 + j;
-        const f2 d2 = *reinterpret_cast<const f2*>(&sD[k * CB + cw]);
-        const f2 du = mul2(d2, *reinterpret_cast<const f2*>(&sU[k * CB + cw]));
-        if (!OUT) dsum = add2(dsum, d2);
+        const float2 du = sDU[k * CB + cw];
+        const f2 d2 = pack2(du.x, du.x), x2 = pack2(du.y, du.y);
+        if (!OUT) dsum += du.x;
         f2 y = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < M / 2; ++i) {
           const f2 e = ex2_2(mul2(d2, A2[i]));
-          h[i] = fma2(e, h[i], mul2(du, sB[k * SP + sl * 4 + i]));
-          if (OUT) y = fma2(h[i], sC[k * SP + sl * 4 + i], y);
+          h[i] = fma2(e, h[i], mul2(x2, *reinterpret_cast<const f2*>(&sB[k * SP + sl * M + 2 * i])));
+          if (OUT) y = fma2(h[i], *reinterpret_cast<const f2*>(&sC[k * SP + sl * M + 2 * i]), y);
         }
-        if (OUT) unpack2(y, v[2 * j], v[2 * j + 1]);
-      }
-      if (OUT) {
-        // lane sl gets token k0 + sl / 2, channel sl & 1; all lanes have read this u
-        butterfly<SL, 0, SL>(v, lane);
-        float* p = &sU[(k0 + sl / 2) * CB + cw + (sl & 1)];
-        *p = fmaf(skip_y, *p, v[0]);
+        if (OUT) {
+          float lo, hi;
+          unpack2(y, lo, hi);
+          sY[(k * kFwdWarps + threadIdx.x / 32) * 32 + lane] = lo + hi;
+        }
       }
     }
     __syncthreads();
@@ -321,9 +322,13 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs a, int bloc
       Raw<T, EPT, VEC> out;
 #pragma unroll
       for (int i = 0; i < EPT; ++i) {
-        float y = sU[row * CB + col + i];
+        // the groups' sums from another one on in each warp's channels: no bank is read twice
+        float y = skip[i] * uu.get(i);
+#pragma unroll
+        for (int q = 0; q < SL; ++q)
+          y += sY[(row * kFwdWarps + col / L::CH) * 32 + (q + col / L::CH) % SL * L::CH + col % L::CH + i];
         if (a.z) {
-          const float z = gate.get(i);
+          const float z = zz.get(i);
           y *= z * fast_sigmoid(z);
         }
         out.set(i, y);
@@ -337,13 +342,20 @@ __global__ void __launch_bounds__(kThreads) scan_fwd_kernel(ScanArgs a, int bloc
     for (int i = 0; i < EPT; ++i) zero.set(i, 0.0f);
     for (int t = max(t0, len) + row; t < t1; t += TT)
       zero.store(static_cast<T*>(a.y) + (seq + t) * a.D + sc, valid);
-    if (a.state_out && chunk == a.chunks - 1)
+  }
+  float w[M];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        store_pair(a.state_out + (long long)b * a.D * a.S, c, r.c1, sl * 4 + i, a.S, h[i]);
-  } else {
-    store_tile<SL>(a.ends + at, c, r.c1, sl * 4, h);
-    if (sl == 0) store_pair(a.dsum + ((long long)b * a.chunks + chunk) * a.D, c, r.c1, 0, 1, dsum);
+  for (int i = 0; i < M / 2; ++i) unpack2(h[i], w[2 * i], w[2 * i + 1]);
+  if (OUT) {
+    if (a.state_out && chunk == a.chunks - 1 && mine) {
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+        if (sl * M + i < a.S) a.state_out[((long long)b * a.D + c) * a.S + sl * M + i] = w[i];
+    }
+  } else if (mine) {
+#pragma unroll
+    for (int i = 0; i < M; ++i) a.ends[at + i] = w[i];
+    if (sl == 0) a.dsum[((long long)b * a.chunks + chunk) * a.D + c] = dsum;
   }
 }
 
@@ -449,18 +461,21 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
 // Marks, chunk end states, and with more than one chunk the chunk's share of the state gradient
 // in front of it, sum_t (prod_{t' <= t} a_t') C_t g_t. Same tiling as the forward.
 template <typename T, int SL, bool VEC, bool SPLIT>
-__global__ void __launch_bounds__(kThreads) scan_marks_kernel(ScanArgs a, int blocks_per_group) {
-  using L = Tile<SL>;
-  constexpr int TT = L::TT, CB = L::CB, SP = L::SP, EPT = L::EPT;
-  __shared__ __align__(16) float sD[TT * CB], sU[TT * CB], sG[SPLIT ? TT * CB : 4];
-  __shared__ __align__(16) f2 sB[TT * SP], sC[SPLIT ? TT * SP : 2];
+__global__ void __launch_bounds__(kFwdThreads) scan_marks_kernel(ScanArgs a, int blocks_per_group,
+                                                                 bool vec_b, bool vec_c) {
+  using L = FwdTile<SL>;
+  constexpr int TT = L::TT, CB = L::CB, SP = L::SP, EPT = L::EPT, M = L::M;
+  constexpr bool AHEAD = L::BCN <= 2;
+  __shared__ __align__(16) float2 sDU[TT * CB];   // delta; delta u
+  __shared__ __align__(16) float sG[SPLIT ? TT * CB : 4];
+  __shared__ __align__(16) float sB[TT * SP], sC[SPLIT ? TT * SP : 4];
   const Range r = block_channels(blockIdx.x, blocks_per_group, a.D, a.G, CB);
   const int chunk = blockIdx.y, b = blockIdx.z;
   const int len = sequence_length(a.lens, b, a.N);
   const int t0 = chunk * a.chunk, te = min(min(a.N, t0 + a.chunk), len);
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int sl = lane % SL, cw = warp * L::WC + lane / SL * 2;
-  const int c = r.c0 + cw;
+  const int lane = threadIdx.x % 32, sl = lane / L::CH;
+  const int cw = threadIdx.x / 32 * L::CH + lane % L::CH, c = r.c0 + cw;
+  const bool mine = c < r.c1;
   const int row = threadIdx.x / L::TPR, col = threadIdx.x % L::TPR * EPT;
   const int sc = r.c0 + col, valid = min(EPT, r.c1 - sc);
   const long long seq = (long long)b * a.N;
@@ -468,259 +483,495 @@ __global__ void __launch_bounds__(kThreads) scan_marks_kernel(ScanArgs a, int bl
   float bias[EPT];
 #pragma unroll
   for (int i = 0; i < EPT; ++i) bias[i] = a.dt_bias && i < valid ? a.dt_bias[sc + i] : 0.0f;
-  f2 A2[4], h[4], prod[4], share[4], dsum = 0;
-  load_A<SL>(a, c, r.c1, sl * 4, A2);
+  f2 A2[M / 2], h[M / 2], prod[M / 2], share[M / 2];
+  float dsum = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < M / 2; ++i) {
+    const int s = sl * M + 2 * i;
+    const float lo = mine && s < a.S ? a.A[(long long)c * a.S + s] : 0.0f;
+    const float hi = mine && s + 1 < a.S ? a.A[(long long)c * a.S + s + 1] : 0.0f;
+    A2[i] = pack2(lo * kLog2e, hi * kLog2e);
     h[i] = share[i] = 0;
-    prod[i] = pack2(1.0f, 1.0f);
+    prod[i] = both(1.0f);
   }
   Raw<T, EPT, VEC> ru, rd, rz, rg;
+  RowsBC<T, SL> rb, rc;
+  const T* pB = static_cast<const T*>(a.Bm) + seq * a.b_row + (long long)r.g * a.S;
+  const T* pC = static_cast<const T*>(a.Cm) + seq * a.c_row + (long long)r.g * a.S;
+  auto fetch_bc = [&](int t) {
+    rb.load(pB + t * a.b_row, a.b_row, a.S, vec_b, te - t);
+    if (SPLIT) rc.load(pC + t * a.c_row, a.c_row, a.S, vec_c, te - t);
+  };
   auto fetch = [&](int t) {
     const int k = t + row, ok = k < te ? valid : 0;
     ru.load(static_cast<const T*>(a.u) + (seq + k) * a.u_row + sc, ok);
     rd.load(static_cast<const T*>(a.dt) + (seq + k) * a.dt_row + sc, ok);
     if (SPLIT) rg.load(static_cast<const T*>(a.dy) + (seq + k) * a.D + sc, ok);
     if (SPLIT && a.z) rz.load(static_cast<const T*>(a.z) + (seq + k) * a.z_row + sc, ok);
+    if (AHEAD) fetch_bc(t);
   };
-  if (t0 < te) fetch(t0);
+  const auto store_states = [&](float* p, const f2 (&v)[M / 2]) {   // p: the channel's row
+    float w[M];
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) unpack2(v[i], w[2 * i], w[2 * i + 1]);
+    if (mine) store_vec<float, M>(p + sl * M, w);
+  };
+  fetch(t0);
   for (int t = t0; t < te; t += TT) {
     const bool on = t + row < te;
+    if (!AHEAD) fetch_bc(t);
+    rb.store(sB);
+    if (SPLIT) rc.store(sC);
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const float raw = rd.get(i) + bias[i];
-      sD[row * CB + col + i] = on && i < valid ? (a.softplus ? softplus(raw) : raw) : 0.0f;
-      sU[row * CB + col + i] = ru.get(i);
+    for (int i = 0; i < EPT; i += 2) {
+      f2 d = add2(pack2(rd.get(i), rd.get(i + 1)), pack2(bias[i], bias[i + 1]));
+      if (a.softplus) d = softplus2(d);
+      if (!on) d = 0;
+      float d0, d1;
+      unpack2(d, d0, d1);
+      store_vec<float, 4>(&sDU[row * CB + col + i].x, {d0, d0 * ru.get(i), d1, d1 * ru.get(i + 1)});
       if (SPLIT) {
-        float g = rg.get(i);
+        float g0 = rg.get(i), g1 = rg.get(i + 1);
         if (a.z) {
-          const float z = rz.get(i);
-          g *= z * fast_sigmoid(z);
+          const float z0 = rz.get(i), z1 = rz.get(i + 1);
+          g0 *= z0 * fast_sigmoid(z0);
+          g1 *= z1 * fast_sigmoid(z1);
         }
-        sG[row * CB + col + i] = g;
+        store_vec<float, 2>(&sG[row * CB + col + i], {g0, g1});
       }
     }
-    stage_bc<T, SL, TT>(sB, a.Bm, a.b_row, a, b, r.g, t, te - t);
-    if (SPLIT) stage_bc<T, SL, TT>(sC, a.Cm, a.c_row, a, b, r.g, t, te - t);
     __syncthreads();
-    if (t + TT < te) fetch(t + TT);
+    fetch(t + TT);
 #pragma unroll 1
     for (int k0 = 0; k0 < TT && t + k0 < te; k0 += kScanSub) {
       const long long mark = (long long)b * subs + (t + k0) / kScanSub;
-      store_tile<SL>(a.marks + mark * a.D * SP, c, r.c1, sl * 4, h);
-      if (sl == 0) store_pair(a.msum + mark * a.D, c, r.c1, 0, 1, dsum);
+      store_states(a.marks + (mark * a.D + c) * SP, h);
+      if (sl == 0 && mine) a.msum[mark * a.D + c] = dsum;
 #pragma unroll
       for (int j = 0; j < kScanSub; ++j) {
         const int k = k0 + j;
-        const f2 d2 = *reinterpret_cast<const f2*>(&sD[k * CB + cw]);
-        const f2 du = mul2(d2, *reinterpret_cast<const f2*>(&sU[k * CB + cw]));
-        dsum = add2(dsum, d2);
-        f2 g2 = 0;
-        if (SPLIT) g2 = *reinterpret_cast<const f2*>(&sG[k * CB + cw]);
+        const float2 du = sDU[k * CB + cw];
+        const f2 d2 = both(du.x), x2 = both(du.y), g2 = both(SPLIT ? sG[k * CB + cw] : 0.0f);
+        dsum += du.x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < M / 2; ++i) {
           const f2 e = ex2_2(mul2(d2, A2[i]));
-          h[i] = fma2(e, h[i], mul2(du, sB[k * SP + sl * 4 + i]));
+          h[i] = fma2(e, h[i], mul2(x2, *reinterpret_cast<const f2*>(&sB[k * SP + sl * M + 2 * i])));
           if (SPLIT) {
             prod[i] = mul2(prod[i], e);
-            share[i] = fma2(prod[i], mul2(g2, sC[k * SP + sl * 4 + i]), share[i]);
+            share[i] = fma2(prod[i], mul2(g2, *reinterpret_cast<const f2*>(&sC[k * SP + sl * M + 2 * i])), share[i]);
           }
         }
       }
     }
     __syncthreads();
   }
-  const long long bk = (long long)b * a.chunks + chunk, at = bk * a.D * SP;
-  store_tile<SL>(a.ends + at, c, r.c1, sl * 4, h);
-  if (SPLIT) store_tile<SL>(a.back + at, c, r.c1, sl * 4, share);
-  if (sl == 0) store_pair(a.dsum + bk * a.D, c, r.c1, 0, 1, dsum);
+  const long long at = ((long long)b * a.chunks + chunk) * a.D + c;
+  store_states(a.ends + at * SP, h);
+  if (SPLIT) store_states(a.back + at * SP, share);
+  if (sl == 0 && mine) a.dsum[at] = dsum;
 }
 
-template <int SL> struct BwdTile : Tile<SL> {
-  static constexpr int EPT = kScanSub * Tile<SL>::CB / kThreads;   // 16 / SL
-  static constexpr int TPR = Tile<SL>::CB / EPT;
+// The main pass's tile: a lane holds 2 channels x 4 states (8 recurrences, so that the sums
+// over the channels, whose shuffles cost most, run over fewer lanes), lane = state group * CL +
+// channel pair.
+template <int SL> struct BwdTile {
+  static constexpr int SP = 4 * SL;
+  static constexpr int CL = 32 / SL;                       // channel pairs of a warp
+  static constexpr int WC = 2 * CL;                        // channels of a warp
+  static constexpr int CB = kWarps * WC;                   // channels of a block
+  static constexpr int EPT = kScanSub * CB / kThreads;     // channels a thread stages (one token)
+  static constexpr int TPR = CB / EPT;                     // threads of a token's row
 };
 
-// The main pass of one chunk, 8 tokens at a time from its end. grid (channel blocks, chunks, B).
-template <typename T, int SL, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, int blocks_per_group) {
+// Shared memory of a main-pass block. `raw` holds the operands of the 8 tokens as they are in
+// memory (u, dt, z, dy), for the staging and again for the per-channel results: registers are
+// what the recurrences need.
+template <typename T, int SL> struct BwdShared {
   using L = BwdTile<SL>;
-  constexpr int K = kScanSub, CB = L::CB, SP = L::SP, EPT = L::EPT, CL = L::CL;
-  __shared__ __align__(16) float sD[K * CB], sU[K * CB], sG[K * CB];
-  __shared__ __align__(16) float sP[K * CB], sX[K * CB], sY[K * CB];   // sums over the states
-  __shared__ __align__(16) f2 sB[K * SP], sC[K * SP];
-  __shared__ float sW[kWarps][K][2 * SP];                               // sums over the channels
+  static constexpr int K = kScanSub, CB = L::CB, SP = L::SP;
+  float4 du[K * CB / 2];            // channel pair: delta, delta, delta u, delta u
+  float4 px[K * kThreads];          // sums over a lane's 4 states: p and x of both channels
+  float2 y[K * kThreads];           // C h of both channels
+  float4 start[2 * kThreads];       // the chunk's start state, lane by lane
+  float4 marks[2][CB * SL];         // states before the 8 tokens, 4 per entry, see mark_slot
+  alignas(16) float g[K * CB];
+  float B[K * SP], C[K * SP];
+  float w[kWarps][K][2 * SP];       // sums over a warp's channels
+  float acc[2][K * CB];             // dD and ddt_bias of each staging slot
+  float bias[CB], skip[CB];         // dt_bias and D, zeros where absent
+  float msum[2][CB];
+  alignas(16) T raw[2][4][K * CB];
+  alignas(16) T rawbc[2][2][K * SP];
+};
+
+// Shared memory read before is read again after this, not kept in registers: the passes over the
+// 8 tokens read the same operands, and the compiler would hold them (and the exponentials of
+// the first 4 tokens) at the price of spilling the states.
+__device__ __forceinline__ void read_again() { asm volatile("" ::: "memory"); }
+
+// Where a lane's sums lie among its warp's 32 in BwdShared::px and y: even channel pairs first,
+// odd ones first in odd warps, so that the threads which add them up (two pairs of two warps
+// in a quarter warp) read different banks.
+template <int CL>
+__device__ __forceinline__ int sum_slot(int warp, int sl, int cl) {
+  return warp * 32 + sl * CL + cl / 2 + (((cl ^ warp) & 1) ? CL / 2 : 0);
+}
+
+// Where 4 states (group sl) of channel ch lie in BwdShared::marks: rotated by the channel pair,
+// for the lanes of a quarter warp read one group of different pairs.
+template <int SL>
+__device__ __forceinline__ int mark_slot(int ch, int sl) {
+  return ch * SL + ((sl + ch / 2) & (SL - 1));
+}
+
+// The main pass of one chunk, 8 tokens at a time from its end. grid (channel blocks, chunks, B).
+// Of the 8 tokens only 4 at a time hold their a_t and h_t in registers: the first 4 are run
+// through once for the state in front of the last 4, and again when their turn comes. That is
+// half an exponential more per state, and three blocks per SM instead of two.
+// VEC: the next 8 tokens' operands come by asynchronous copies under this one's arithmetic.
+template <typename T, int SL, bool VEC>
+__global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArgs a, int blocks_per_group,
+                                                                         bool vec_b, bool vec_c) {
+  using L = BwdTile<SL>;
+  constexpr int K = kScanSub, H = K / 2, CB = L::CB, SP = L::SP, EPT = L::EPT, CL = L::CL;
+  extern __shared__ __align__(16) unsigned char smem[];
+  BwdShared<T, SL>& sm = *reinterpret_cast<BwdShared<T, SL>*>(smem);
   const Range r = block_channels(blockIdx.x, blocks_per_group, a.D, a.G, CB);
   const int chunk = blockIdx.y, b = blockIdx.z;
   const int len = sequence_length(a.lens, b, a.N);
   const int t0 = chunk * a.chunk, t1 = min(a.N, t0 + a.chunk), te = min(t1, len);
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int sl = lane % SL, cl = lane / SL, cw = warp * L::WC + cl * 2;
-  const int c = r.c0 + cw;
-  const int row = threadIdx.x / L::TPR, col = threadIdx.x % L::TPR * EPT;
+  const int sl = lane / CL, cl = lane % CL, pair = warp * CL + cl;   // state group; channel pair
+  const int c = r.c0 + 2 * pair;
+  const int row = threadIdx.x / L::TPR, col = threadIdx.x % L::TPR * EPT, slot = row * CB + col;
   const int sc = r.c0 + col, valid = min(EPT, r.c1 - sc);
   const long long seq = (long long)b * a.N;
   const int subs = (a.N + K - 1) / K;
   const int cb = blockIdx.x % blocks_per_group;
   float* bcpart = a.bcpart + (((long long)cb * a.B + b) * a.N * a.G + r.g) * 2 * SP;
-  float bias[EPT], skip[EPT], accD[EPT], accb[EPT];
+  f2 A2[2][2], carry[2][2], dA[2][2];   // [channel][state pair]
+  const long long bk = (long long)b * a.chunks + chunk;
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) {
-    bias[i] = a.dt_bias && i < valid ? a.dt_bias[sc + i] : 0.0f;
-    skip[i] = a.Dskip && i < valid ? a.Dskip[sc + i] : 0.0f;
-    accD[i] = accb[i] = 0.0f;
+  for (int z = 0; z < 2; ++z) {
+    float w[4] = {}, g[4] = {}, v[4];
+    if (c + z < r.c1) {
+      load_vec<float, 4>(a.ends + (bk * a.D + c + z) * SP + sl * 4, w);
+      load_vec<float, 4>(a.back + (bk * a.D + c + z) * SP + sl * 4, g);
+    }
+    sm.start[z * kThreads + threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int s = sl * 4 + i;
+      v[i] = c + z < r.c1 && s < a.S ? a.A[(long long)(c + z) * a.S + s] * kLog2e : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      carry[z][i] = pack2(g[2 * i], g[2 * i + 1]);
+      A2[z][i] = pack2(v[2 * i], v[2 * i + 1]);
+      dA[z][i] = 0;
+    }
   }
-  f2 A2[4], carry[4], dA[4];
-  load_A<SL>(a, c, r.c1, sl * 4, A2);
-  const long long bk = (long long)b * a.chunks + chunk, at = bk * a.D * SP;
-  load_tile<SL>(a.back + at, c, r.c1, sl * 4, carry);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dA[i] = 0;
-  Raw<T, EPT, VEC> nu, nd, nz, ng;
-  auto fetch = [&](int t) {
-    const int k = t + row, ok = k < te ? valid : 0;
-    nu.load(static_cast<const T*>(a.u) + (seq + k) * a.u_row + sc, ok);
-    nd.load(static_cast<const T*>(a.dt) + (seq + k) * a.dt_row + sc, ok);
-    ng.load(static_cast<const T*>(a.dy) + (seq + k) * a.D + sc, ok);
-    if (a.z) nz.load(static_cast<const T*>(a.z) + (seq + k) * a.z_row + sc, ok);
+  for (int i = 0; i < EPT; ++i) sm.acc[0][slot + i] = sm.acc[1][slot + i] = 0.0f;
+  for (int i = threadIdx.x; i < CB; i += kThreads) {
+    const bool in = r.c0 + i < r.c1;
+    sm.bias[i] = a.dt_bias && in ? a.dt_bias[r.c0 + i] : 0.0f;
+    sm.skip[i] = a.Dskip && in ? a.Dskip[r.c0 + i] : 0.0f;
+  }
+  const int lane_sum = sum_slot<CL>(warp, sl, cl);
+
+  const T* const src[4] = {static_cast<const T*>(a.u) + sc, static_cast<const T*>(a.dt) + sc,
+                           static_cast<const T*>(a.z) + sc, static_cast<const T*>(a.dy) + sc};
+  Raw<T, EPT, false> regs[VEC ? 1 : 4];
+  // the operands of the 8 tokens from t on (none in front of t0 or behind te) into buffer `buf`
+  const auto fetch = [&](int t, int buf) {
+    const int k = t + row, ok = t >= t0 && k < te ? valid : 0;
+    const long long at[4] = {(seq + k) * a.u_row, (seq + k) * a.dt_row, (seq + k) * a.z_row, (seq + k) * a.D};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i == 2 && !a.z) continue;
+      if constexpr (VEC) {
+        constexpr int BYTES = EPT * sizeof(T) > 16 ? 16 : EPT * (int)sizeof(T);
+#pragma unroll
+        for (int q = 0; q < EPT * (int)sizeof(T) / BYTES; ++q)
+          copy_async<BYTES>(&sm.raw[buf][i][slot + q * BYTES / sizeof(T)], src[i] + at[i] + q * BYTES / sizeof(T), ok > 0);
+      } else {
+        regs[i].load(src[i] + at[i], ok);
+      }
+    }
+    const long long mark = ((long long)b * subs + t / K) * a.D + r.c0;
+    const bool in = t >= t0 && t < te;
+    for (int i = threadIdx.x; i < CB * SL; i += kThreads) {
+      const int ch = i / SL;
+      copy_async<16>(&sm.marks[buf][mark_slot<SL>(ch, i % SL)], a.marks + mark * SP + i * 4,
+                     in && r.c0 + ch < r.c1);
+    }
+    if (threadIdx.x < CB)
+      copy_async<4>(&sm.msum[buf][threadIdx.x], a.msum + mark + threadIdx.x, in && r.c0 + threadIdx.x < r.c1);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const long long stride = w ? a.c_row : a.b_row;
+      const T* p = static_cast<const T*>(w ? a.Cm : a.Bm) + (seq + t) * stride + (long long)r.g * a.S;
+      if (w ? vec_c : vec_b) {
+        for (int i = threadIdx.x; i < K * SL; i += kThreads) {
+          const int q = i / SL, s = i % SL * 4;
+          copy_async<4 * sizeof(T)>(&sm.rawbc[buf][w][i * 4], p + q * stride + s, t >= t0 && t + q < te && s < a.S);
+        }
+      } else {
+        for (int i = threadIdx.x; i < K * SP; i += kThreads) {
+          const int q = i / SP, s = i % SP;
+          sm.rawbc[buf][w][i] = t >= t0 && t + q < te && s < a.S ? p[q * stride + s] : from_f32<T>(0.0f);
+        }
+      }
+    }
   };
   const int last = te > t0 ? (te - 1 - t0) / K * K + t0 : t0 - K;   // first token of the last 8
-  if (last >= t0) fetch(last);
-  for (int t = last; t >= t0; t -= K) {
-    const Raw<T, EPT, VEC> ru = nu, rd = nd, rz = nz, rg = ng;
+  int buf = 0;
+  if (last >= t0) fetch(last, 0);
+  for (int t = last; t >= t0; t -= K, buf ^= 1) {
     const bool on = t + row < te;
+    if constexpr (!VEC) {
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) {
-      const float raw = rd.get(i) + bias[i];
-      sD[row * CB + col + i] = on && i < valid ? (a.softplus ? softplus(raw) : raw) : 0.0f;
-      sU[row * CB + col + i] = ru.get(i);
-      float g = rg.get(i);
-      if (a.z) {
-        const float z = rz.get(i);
-        g *= z * fast_sigmoid(z);
-      }
-      sG[row * CB + col + i] = g;
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) sm.raw[buf][i][slot + e] = regs[i].t[e];
     }
-    stage_bc<T, SL, K>(sB, a.Bm, a.b_row, a, b, r.g, t, te - t);
-    stage_bc<T, SL, K>(sC, a.Cm, a.c_row, a, b, r.g, t, te - t);
+    copies_wait();
+    __syncthreads();   // also: everybody is done with the tile before
+    fetch(t - K, buf ^ 1);
+    // stage: delta, delta u and the gated dy in fp32, B and C in fp32
+    {
+      float u[EPT], raw[EPT], g[EPT], z[EPT], bias[EPT];
+      load_vec<float, EPT>(&sm.bias[col], bias);
+      load_vec<T, EPT>(&sm.raw[buf][0][slot], u);
+      load_vec<T, EPT>(&sm.raw[buf][1][slot], raw);
+      load_vec<T, EPT>(&sm.raw[buf][3][slot], g);
+      if (a.z) load_vec<T, EPT>(&sm.raw[buf][2][slot], z);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        raw[i] += bias[i];
+        if (a.z) g[i] *= z[i] * fast_sigmoid(z[i]);
+      }
+      if constexpr (EPT == 1) {
+        const float d = on ? (a.softplus ? softplus(raw[0]) : raw[0]) : 0.0f;
+        float* p = reinterpret_cast<float*>(&sm.du[slot / 2]) + slot % 2;
+        p[0] = d;
+        p[2] = d * u[0];
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPT; i += 2) {
+          f2 d = pack2(raw[i], raw[i + 1]);
+          if (a.softplus) d = softplus2(d);
+          if (!on) d = 0;
+          float d0, d1;
+          unpack2(d, d0, d1);
+          sm.du[(slot + i) / 2] = make_float4(d0, d1, d0 * u[i], d1 * u[i + 1]);
+        }
+      }
+      store_vec<float, EPT>(&sm.g[slot], g);
+      for (int i = threadIdx.x; i < 2 * K * SL; i += kThreads) {
+        const int w = i / (K * SL), at = i % (K * SL) * 4;
+        float f[4];
+        load_vec<T, 4>(&sm.rawbc[buf][w][at], f);
+        store_vec<float, 4>(w ? &sm.C[at] : &sm.B[at], f);
+      }
+    }
     __syncthreads();
-    if (t - K >= t0) fetch(t - K);
 
     // the state in front of the 8 tokens: the mark plus the chunk's decayed start state
-    f2 h0[4], h[K][4], e[K][4];
-    {
-      const long long mark = (long long)b * subs + t / K;
-      const f2 m2 = load_pair(a.msum + mark * a.D, c, r.c1, 0, 1);
-      f2 start[4];
-      load_tile<SL>(a.ends + at, c, r.c1, sl * 4, start);
-      load_tile<SL>(a.marks + mark * a.D * SP, c, r.c1, sl * 4, h0);
+    f2 h0[2][2], h4[2][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h0[i] = fma2(ex2_2(mul2(m2, A2[i])), start[i], h0[i]);
+    for (int z = 0; z < 2; ++z) {
+      const float4 S4 = sm.start[z * kThreads + threadIdx.x];
+      const float4 M4 = sm.marks[buf][mark_slot<SL>(2 * pair + z, sl)];
+      const f2 m2 = both(sm.msum[buf][2 * pair + z]);
+      h4[z][0] = h0[z][0] = fma2(ex2_2(mul2(m2, A2[z][0])), pack2(S4.x, S4.y), pack2(M4.x, M4.y));
+      h4[z][1] = h0[z][1] = fma2(ex2_2(mul2(m2, A2[z][1])), pack2(S4.z, S4.w), pack2(M4.z, M4.w));
     }
-    constexpr int YB = SL / 2;             // tokens whose C h sums leave together
-    float vy[SL];
+    // one token forward: its a_t, and the state behind it in place
+    const auto advance = [&](int k, f2 (&e)[2][2], f2 (&h)[2][2]) {
+      read_again();
+      const float4 du = sm.du[k * (CB / 2) + pair];
+      const float4 B4 = *reinterpret_cast<const float4*>(&sm.B[k * SP + sl * 4]);
+      const f2 B2[2] = {pack2(B4.x, B4.y), pack2(B4.z, B4.w)};
+      const f2 d2[2] = {both(du.x), both(du.y)}, x2[2] = {both(du.z), both(du.w)};
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const f2 d2 = *reinterpret_cast<const f2*>(&sD[k * CB + cw]);
-      const f2 du = mul2(d2, *reinterpret_cast<const f2*>(&sU[k * CB + cw]));
-      f2 y = 0;
+      for (int z = 0; z < 2; ++z)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        e[k][i] = ex2_2(mul2(d2, A2[i]));
-        h[k][i] = fma2(e[k][i], k ? h[k - 1][i] : h0[i], mul2(du, sB[k * SP + sl * 4 + i]));
-        y = fma2(h[k][i], sC[k * SP + sl * 4 + i], y);
-      }
-      if (a.z) {
-        unpack2(y, vy[2 * (k % YB)], vy[2 * (k % YB) + 1]);
-        if (k % YB == YB - 1) {
-          butterfly<SL, 0, SL>(vy, lane);
-          sY[(k / YB * YB + sl / 2) * CB + cw + (sl & 1)] = vy[0];
+        for (int i = 0; i < 2; ++i) {
+          e[z][i] = ex2_2(mul2(d2[z], A2[z][i]));
+          h[z][i] = fma2(e[z][i], h[z][i], mul2(x2[z], B2[i]));
         }
-      }
-    }
-    constexpr int RB = SL > 4 ? SL / 4 : 1;   // tokens whose p and x sums leave together
-    constexpr int RV = 4 * RB;
-    float vr[RV];
+    };
+    const auto read_out = [&](int k, const f2 (&h)[2][2]) {
+      const float4 C4 = *reinterpret_cast<const float4*>(&sm.C[k * SP + sl * 4]);
+      const f2 C2[2] = {pack2(C4.x, C4.y), pack2(C4.z, C4.w)};
+      float y[2];
 #pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-      const f2 d2 = *reinterpret_cast<const f2*>(&sD[k * CB + cw]);
-      const f2 g2 = *reinterpret_cast<const f2*>(&sG[k * CB + cw]);
-      const f2 du = mul2(d2, *reinterpret_cast<const f2*>(&sU[k * CB + cw]));
-      f2 sp = 0, sx = 0;
-      float v[8];                              // dB, dC of the lane's 4 states
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f2 dh = fma2(g2, sC[k * SP + sl * 4 + i], carry[i]);
-        carry[i] = mul2(e[k][i], dh);
-        const f2 p = mul2(carry[i], k ? h[k - 1][i] : h0[i]);
-        sp = fma2(A2[i], p, sp);
-        dA[i] = fma2(d2, p, dA[i]);
-        sx = fma2(dh, sB[k * SP + sl * 4 + i], sx);
+      for (int z = 0; z < 2; ++z) {
         float lo, hi;
-        unpack2(mul2(dh, du), lo, hi);
-        v[i] = lo + hi;
-        unpack2(mul2(g2, h[k][i]), lo, hi);
-        v[4 + i] = lo + hi;
+        unpack2(fma2(h[z][1], C2[1], mul2(h[z][0], C2[0])), lo, hi);
+        y[z] = lo + hi;
       }
-      // over the states: p and x of both channels
-      const int j = (K - 1 - k) % RB;
-      unpack2(sp, vr[4 * j], vr[4 * j + 1]);
-      unpack2(sx, vr[4 * j + 2], vr[4 * j + 3]);
-      if (j == RB - 1) {
-        butterfly<SL, 0, RV>(vr, lane);
+      sm.y[k * kThreads + lane_sum] = make_float2(y[0], y[1]);
+    };
 #pragma unroll
-        for (int q = 0; q < RV / SL; ++q) {
-          const int id = sl * (RV / SL) + q;    // token in the batch, then p / x, then channel
-          float* dst = id & 2 ? sX : sP;
-          dst[(k + RB - 1 - id / 4) * CB + cw + (id & 1)] = vr[q];
-        }
+    for (int k = 0; k < H; ++k) {
+      f2 e[2][2];
+      advance(k, e, h4);
+      if (a.z) read_out(k, h4);
+    }
+#pragma unroll
+    for (int half = 1; half >= 0; --half) {
+      f2 e[H][2][2], h[H][2][2];
+#pragma unroll
+      for (int k = 0; k < H; ++k) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) h[k][z][i] = k ? h[k - 1][z][i] : half ? h4[z][i] : h0[z][i];
+        advance(half * H + k, e[k], h[k]);
+        if (half && a.z) read_out(half * H + k, h[k]);
       }
-      // over the channels: lane cl gets the sums from index cl * 8 / CL on
-      butterfly<CL, (SL == 2 ? 1 : SL == 4 ? 2 : SL == 8 ? 3 : 4), 8>(v, lane);
-      constexpr int OV = CL >= 8 ? 1 : 8 / CL;
-      if (CL <= 8 || cl % (CL / 8 > 0 ? CL / 8 : 1) == 0) {
 #pragma unroll
-        for (int q = 0; q < OV; ++q) {
-          const int id = CL >= 8 ? cl / (CL / 8 > 0 ? CL / 8 : 1) : cl * OV + q;
-          sW[warp][k][(id / 4) * SP + sl * 4 + id % 4] = v[q];
+      for (int j = H - 1; j >= 0; --j) {
+        const int k = half * H + j;
+        read_again();
+        const float4 du = sm.du[k * (CB / 2) + pair];
+        const float2 g = *reinterpret_cast<const float2*>(&sm.g[k * CB + 2 * pair]);
+        const float4 B4 = *reinterpret_cast<const float4*>(&sm.B[k * SP + sl * 4]);
+        const float4 C4 = *reinterpret_cast<const float4*>(&sm.C[k * SP + sl * 4]);
+        const f2 B2[2] = {pack2(B4.x, B4.y), pack2(B4.z, B4.w)}, C2[2] = {pack2(C4.x, C4.y), pack2(C4.z, C4.w)};
+        const f2 d2[2] = {both(du.x), both(du.y)}, x2[2] = {both(du.z), both(du.w)};
+        const f2 g2[2] = {both(g.x), both(g.y)};
+        f2 sp[2], sx[2], sb[2], sc2[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const f2 dh = fma2(g2[z], C2[i], carry[z][i]);
+            carry[z][i] = mul2(e[j][z][i], dh);
+            const f2 p = mul2(carry[z][i], j ? h[j - 1][z][i] : half ? h4[z][i] : h0[z][i]);
+            dA[z][i] = fma2(d2[z], p, dA[z][i]);
+            sp[z] = i ? fma2(A2[z][i], p, sp[z]) : mul2(A2[z][i], p);
+            sx[z] = i ? fma2(dh, B2[i], sx[z]) : mul2(dh, B2[i]);
+            sb[i] = z ? fma2(dh, x2[z], sb[i]) : mul2(dh, x2[z]);
+            sc2[i] = z ? fma2(g2[z], h[j][z][i], sc2[i]) : mul2(g2[z], h[j][z][i]);
+          }
+        // over the states: left to the per-channel pass below
+        float4 px;
+        float lo, hi;
+        unpack2(sp[0], lo, hi);
+        px.x = lo + hi;
+        unpack2(sp[1], lo, hi);
+        px.y = lo + hi;
+        unpack2(sx[0], lo, hi);
+        px.z = lo + hi;
+        unpack2(sx[1], lo, hi);
+        px.w = lo + hi;
+        sm.px[k * kThreads + lane_sum] = px;
+        // over the warp's channels: lane cl gets the sums from index cl * 8 / CL on
+        float v[8];                     // dB, dC of the lane's 4 states
+        unpack2(sb[0], v[0], v[1]);
+        unpack2(sb[1], v[2], v[3]);
+        unpack2(sc2[0], v[4], v[5]);
+        unpack2(sc2[1], v[6], v[7]);
+        butterfly<CL, 0, 8>(v, lane);
+        constexpr int SHARE = CL > 8 ? CL / 8 : 1, OV = CL > 8 ? 1 : 8 / CL;
+        if (cl % SHARE == 0) {
+#pragma unroll
+          for (int q = 0; q < OV; ++q) {
+            const int id = cl / SHARE * OV + q;
+            sm.w[warp][k][(id / 4) * SP + sl * 4 + id % 4] = v[q];
+          }
         }
       }
     }
     __syncthreads();
     // per (token, channel)
     if (on) {
+      float u[EPT], raw[EPT], dy[EPT], z[EPT], p[EPT], x[EPT], y[EPT], delta[EPT];
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) p[i] = x[i] = y[i] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPT; i += 2) {
+        const int ch = col + i;
+#pragma unroll
+        for (int q = 0; q < SL; ++q) {
+          const int at = row * kThreads + sum_slot<CL>(ch / L::WC, q, ch % L::WC / 2);
+          const float4 v = sm.px[at];
+          const float2 w = a.z ? sm.y[at] : make_float2(0.0f, 0.0f);
+          if constexpr (EPT == 1) {
+            p[0] += ch % 2 ? v.y : v.x;
+            x[0] += ch % 2 ? v.w : v.z;
+            y[0] += ch % 2 ? w.y : w.x;
+          } else {
+            p[i] += v.x;
+            p[i + 1] += v.y;
+            x[i] += v.z;
+            x[i + 1] += v.w;
+            y[i] += w.x;
+            y[i + 1] += w.y;
+          }
+        }
+        const float4 du = sm.du[(slot + i) / 2];
+        if constexpr (EPT == 1) {
+          delta[0] = ch % 2 ? du.y : du.x;
+        } else {
+          delta[i] = du.x;
+          delta[i + 1] = du.y;
+        }
+      }
+      float g[EPT], skip[EPT], bias[EPT], acc[2][EPT];
+      load_vec<T, EPT>(&sm.raw[buf][0][slot], u);
+      load_vec<T, EPT>(&sm.raw[buf][1][slot], raw);
+      load_vec<T, EPT>(&sm.raw[buf][3][slot], dy);
+      if (a.z) load_vec<T, EPT>(&sm.raw[buf][2][slot], z);
+      load_vec<float, EPT>(&sm.g[slot], g);
+      load_vec<float, EPT>(&sm.bias[col], bias);
+      load_vec<float, EPT>(&sm.skip[col], skip);
+      load_vec<float, EPT>(&sm.acc[0][slot], acc[0]);
+      load_vec<float, EPT>(&sm.acc[1][slot], acc[1]);
       Raw<T, EPT, VEC> odu, odt, odz;
 #pragma unroll
       for (int i = 0; i < EPT; ++i) {
-        const int o = row * CB + col + i;
-        const float g = sG[o], u = sU[o], x = sX[o];
-        odu.set(i, fmaf(skip[i], g, sD[o] * x));
-        float dd = fmaf(u, x, sP[o] * kLn2);
-        if (a.softplus) dd *= fast_sigmoid(rd.get(i) + bias[i]);
+        odu.set(i, fmaf(skip[i], g[i], delta[i] * x[i]));
+        float dd = fmaf(u[i], x[i], p[i] * kLn2);
+        if (a.softplus) dd *= fast_sigmoid(raw[i] + bias[i]);
         odt.set(i, dd);
-        accD[i] = fmaf(g, u, accD[i]);
-        accb[i] += i < valid ? dd : 0.0f;
+        acc[0][i] = fmaf(g[i], u[i], acc[0][i]);
+        acc[1][i] += dd;
         if (a.z) {
-          const float z = rz.get(i), sg = fast_sigmoid(z);
-          odz.set(i, rg.get(i) * fmaf(skip[i], u, sY[o]) * sg * fmaf(z, 1.0f - sg, 1.0f));
+          const float sg = fast_sigmoid(z[i]);
+          odz.set(i, dy[i] * fmaf(skip[i], u[i], y[i]) * sg * fmaf(z[i], 1.0f - sg, 1.0f));
         }
       }
+      store_vec<float, EPT>(&sm.acc[0][slot], acc[0]);
+      store_vec<float, EPT>(&sm.acc[1][slot], acc[1]);
       const long long o = (seq + t + row) * a.D + sc;
       odu.store(static_cast<T*>(a.du) + o, valid);
       odt.store(static_cast<T*>(a.ddt) + o, valid);
       if (a.z) odz.store(static_cast<T*>(a.dz) + o, valid);
     }
     // per (token, state): the block's channels
-    for (int i = threadIdx.x; i < K * 2 * SP; i += kThreads) {
-      const int k = i / (2 * SP), q = i % (2 * SP);
+    for (int i = threadIdx.x; i < K * 2 * SL; i += kThreads) {
+      const int k = i / (2 * SL), q = i % (2 * SL) * 4;
       if (t + k < te) {
-        float v = sW[0][k][q];
+        float v[4];
+        load_vec<float, 4>(&sm.w[0][k][q], v);
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) v += sW[w][k][q];
-        bcpart[(long long)(t + k) * a.G * 2 * SP + q] = v;
+        for (int w = 1; w < kWarps; ++w) {
+          float f[4];
+          load_vec<float, 4>(&sm.w[w][k][q], f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += f[e];
+        }
+        store_vec<float, 4>(&bcpart[(long long)(t + k) * a.G * 2 * SP + q], v);
       }
     }
   }
+  copies_wait();   // the copies in front of t0 are empty, but in flight
   // rows behind the sequence's end
   Raw<T, EPT, VEC> zero;
 #pragma unroll
@@ -734,26 +985,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(ScanArgs a, int b
   for (int i = threadIdx.x; i < (t1 - max(t0, len)) * 2 * SP; i += kThreads)
     bcpart[(long long)(max(t0, len) + i / (2 * SP)) * a.G * 2 * SP + i % (2 * SP)] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    store_pair(a.apart + bk * a.D * a.S, c, r.c1, sl * 4 + i, a.S, dA[i]);
-    if (a.dstate_in && chunk == 0)
-      store_pair(a.dstate_in + (long long)b * a.D * a.S, c, r.c1, sl * 4 + i, a.S, carry[i]);
-  }
-  // dD and ddt_bias: the 8 token rows of a channel, through shared memory in a fixed order
-  __syncthreads();
+  for (int z = 0; z < 2; ++z)
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) {
-    sP[row * CB + col + i] = accD[i];
-    sX[row * CB + col + i] = accb[i];
-  }
+    for (int i = 0; i < 2; ++i) {
+      float w[2], g[2];
+      unpack2(dA[z][i], w[0], w[1]);
+      unpack2(carry[z][i], g[0], g[1]);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int s = sl * 4 + 2 * i + q;
+        if (c + z >= r.c1 || s >= a.S) continue;
+        a.apart[(bk * a.D + c + z) * a.S + s] = w[q];
+        if (a.dstate_in && chunk == 0) a.dstate_in[((long long)b * a.D + c + z) * a.S + s] = g[q];
+      }
+    }
+  // dD and ddt_bias: the 8 token rows of a channel in a fixed order
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * CB; i += kThreads) {
-    const int ch = i % CB;
-    const float* src = i < CB ? sP : sX;
+    const int ch = i % CB, which = i / CB;
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v += src[k * CB + ch];
-    if (r.c0 + ch < r.c1) a.dpart[(bk * 2 + i / CB) * a.D + r.c0 + ch] = v;
+    for (int k = 0; k < K; ++k) v += sm.acc[which][k * CB + ch];
+    if (r.c0 + ch < r.c1) a.dpart[(bk * 2 + which) * a.D + r.c0 + ch] = v;
   }
 }
 
@@ -789,25 +1042,39 @@ bool fits(const ScanArgs& a, int ept, int size) {
 
 enum Kernel { ENDS, OUTPUTS, MARKS, MAIN };
 
+// Whether the S states of every row of B or C are whole aligned runs of four.
+bool fits_four(const ScanArgs& a, const void* p, long long row, int size) {
+  return a.S % 4 == 0 && row % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * size) == 0;
+}
+
 template <typename T, int SL, bool VEC, Kernel K>
 cudaError_t launch_kernel(const ScanArgs& a, cudaStream_t s) {
-  const int bpg = scan_channel_blocks(a.D, a.G, a.S);
+  constexpr int CB = K == MAIN ? BwdTile<SL>::CB : FwdTile<SL>::CB;
+  const int bpg = (a.D / a.G + CB - 1) / CB;
+  const bool vb = fits_four(a, a.Bm, a.b_row, sizeof(T)), vc = fits_four(a, a.Cm, a.c_row, sizeof(T));
   const dim3 grid(bpg * a.G, K == ENDS ? a.chunks - 1 : a.chunks, a.B);
-  if constexpr (K == ENDS) scan_fwd_kernel<T, SL, VEC, false><<<grid, kThreads, 0, s>>>(a, bpg);
-  if constexpr (K == OUTPUTS) scan_fwd_kernel<T, SL, VEC, true><<<grid, kThreads, 0, s>>>(a, bpg);
+  if constexpr (K == ENDS || K == OUTPUTS)
+    scan_fwd_kernel<T, SL, VEC, K == OUTPUTS><<<grid, kFwdThreads, 0, s>>>(a, bpg, vb, vc);
   if constexpr (K == MARKS) {
-    if (a.chunks > 1) scan_marks_kernel<T, SL, VEC, true><<<grid, kThreads, 0, s>>>(a, bpg);
-    else scan_marks_kernel<T, SL, VEC, false><<<grid, kThreads, 0, s>>>(a, bpg);
+    if (a.chunks > 1) scan_marks_kernel<T, SL, VEC, true><<<grid, kFwdThreads, 0, s>>>(a, bpg, vb, vc);
+    else scan_marks_kernel<T, SL, VEC, false><<<grid, kFwdThreads, 0, s>>>(a, bpg, vb, vc);
   }
-  if constexpr (K == MAIN) scan_bwd_kernel<T, SL, VEC><<<grid, kThreads, 0, s>>>(a, bpg);
+  if constexpr (K == MAIN) {
+    constexpr size_t bytes = sizeof(BwdShared<T, SL>);
+    const cudaError_t e = cudaFuncSetAttribute(scan_bwd_kernel<T, SL, VEC>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    scan_bwd_kernel<T, SL, VEC><<<grid, kThreads, bytes, s>>>(a, bpg, vb, vc);
+  }
   return cudaGetLastError();
 }
 
 template <typename T, int SL, Kernel K>
 cudaError_t launch_vec(const ScanArgs& a, cudaStream_t s) {
-  constexpr int ept = K == MAIN ? BwdTile<SL>::EPT : Tile<SL>::EPT;
-  return fits(a, ept, sizeof(T)) ? launch_kernel<T, SL, true, K>(a, s)
-                                 : launch_kernel<T, SL, false, K>(a, s);
+  constexpr int ept = K == MAIN ? BwdTile<SL>::EPT : FwdTile<SL>::EPT;
+  if constexpr (K != MAIN || ept * sizeof(T) >= 4)   // an asynchronous copy has 4 bytes at least
+    if (fits(a, ept, sizeof(T))) return launch_kernel<T, SL, true, K>(a, s);
+  return launch_kernel<T, SL, false, K>(a, s);
 }
 
 template <typename T, Kernel K>
@@ -855,17 +1122,30 @@ int scan_channel_blocks(int D, int G, int S) {
   return (D / G + CB - 1) / CB;
 }
 
+// Blocks that run at a time (148 SMs x 7 forward, x 3 backward), and the tokens' worth of work
+// that starting and joining a chunk costs. The forward's first pass doubles its exponentials,
+// so a sequence is cut for it only where whole sequences would leave most SMs idle.
+constexpr long long kFwdSlots = 148 * 7, kBwdSlots = 148 * 3, kChunkCost = 64;
+
 int scan_chunks(int B, int N, int D, int G, int S, bool backward, int* chunk) {
-  const long long warps = (long long)B * G * scan_channel_blocks(D, G, S) * kWarps;
-  const long long want = backward ? 148 * 16 : warps < 148 * 4 ? 148 * 16 : 0;
-  long long n = warps > 0 && want > warps ? (want + warps - 1) / warps : 1;
-  const long long most = (N + 127) / 128;      // pieces of 128 tokens at least
-  if (n > most) n = most;
-  if (n > 4096) n = 4096;
-  if (n < 1) n = 1;
-  long long len = (N + n - 1) / n;
-  len = (len + 31) / 32 * 32;                  // whole staged tiles
-  if (len < 32) len = 32;
+  const int CB = backward ? kWarps * 64 / state_lanes(S) : kFwdWarps * 32 / state_lanes(S);
+  const long long blocks = (long long)B * G * ((D / G + CB - 1) / CB);
+  const long long slots = backward ? kBwdSlots : kFwdSlots;
+  const long long most = std::min<long long>(std::max(1, N / 64), 1024);
+  // rounds of blocks x (tokens of a chunk + cost of a chunk), the least over the counts
+  long long best = 1, least = 0;
+  for (long long n = 1; n <= most; ++n) {
+    const long long len = ((N + n - 1) / n + 31) / 32 * 32;
+    long long time = (std::max<long long>(blocks * n, 1) + slots - 1) / slots * (len + kChunkCost);
+    if (!backward && n > 1) time *= 2;
+    if (n == 1 || time < least) {
+      least = time;
+      best = n;
+    }
+    if (n > 1 && blocks * n > 8 * slots) break;   // balanced to an eighth
+  }
+  long long len = (N + best - 1) / best;
+  len = std::max<long long>((len + 31) / 32 * 32, 32);   // whole staged tiles
   *chunk = (int)len;
   return N > 0 ? (int)((N + len - 1) / len) : 1;
 }
