@@ -7,9 +7,9 @@
 // HBM bound (each element is read and written once), so the layout serves the accesses: a row
 // (token, head) belongs to a group of 1..32 lanes, a lane owns runs of V element pairs and
 // loads both halves of each pair itself, so the rotation needs no exchange and the norm only a
-// shuffle sum. The angles of a token are the same for all heads: a block takes a tile of
-// tokens with all their heads and computes each cosine and sine once into shared memory, from
-// a 64-bit product (fp32 loses far positions: 1e6 * 2^-24 is 0.06 of a radian) reduced to
+// shuffle sum. The angles of a token are the same for all its heads: a group keeps one token
+// and its lanes the cosines and sines of their pairs in registers, each taken once, from a
+// 64-bit product (fp32 loses far positions: 1e6 * 2^-24 is 0.06 of a radian) reduced to
 // [-1/2, 1/2] turns.
 #include "mixer.h"
 #include "mixer_common.cuh"
@@ -17,8 +17,11 @@
 namespace ttt {
 namespace {
 
-constexpr int kHeadThreads = 256;
-constexpr int kMaxTile = 32;
+constexpr int kHeadThreads = 128;
+// Blocks of an SM: what the registers leave (128 a thread forward, 168 backward, where the two
+// weight gradients stay in them), which at 16 lanes a row of 256 elements keeps 16 (12) KB of
+// loads in flight per SM.
+constexpr int kFwdBlocks = 4, kBwdBlocks = 3;
 constexpr double kInvTwoPi = 0.15915494309189533576888;
 
 enum : int { PAIRS_HALVES = 0, PAIRS_INTERLEAVED = 1 };
@@ -39,39 +42,42 @@ __device__ __forceinline__ void pair_at(int p, int rot, int h, int& lo, int& hi)
   }
 }
 
-// V pairs from p on (all of one kind; V > 1 only when every half is whole runs of V).
-template <typename T, int V, int PAIRS>
-__device__ __forceinline__ void load_pairs(const T* row, int p, int rot, int h, float (&a)[V],
-                                           float (&b)[V]) {
-  int lo, hi;
-  pair_at<PAIRS>(p, rot, h, lo, hi);
-  if constexpr (V == 1) {
-    a[0] = to_f32(row[lo]);
-    b[0] = hi < h ? to_f32(row[hi]) : 0.0f;
-  } else if constexpr (PAIRS == PAIRS_INTERLEAVED) {
-    float f[2][V];
-    load_vec<T, V>(row + lo, f[0]);
-    load_vec<T, V>(row + lo + V, f[1]);
+// V pairs from p on as they are in memory (all of one kind; V > 1 only when every half is whole
+// runs of V), or zeros; and as floats.
+template <typename T, int V> struct RawPairs {
+  typename Pack<T, V>::U a, b;
+};
+template <typename T, int V>
+__device__ __forceinline__ void load_raw_pairs(RawPairs<T, V>& r, const T* row, int lo, int hi, bool on, bool on_hi) {
+  load_here(row + lo, on, r.a);
+  load_here(row + hi, on_hi, r.b);
+}
+// 2V neighbours to V first and V second elements.
+template <int V>
+__device__ __forceinline__ void deal(float (&a)[V], float (&b)[V]) {
+  float f[2 * V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      a[i] = f[2 * i / V][2 * i % V];
-      b[i] = f[(2 * i + 1) / V][(2 * i + 1) % V];
-    }
-  } else {
-    load_vec<T, V>(row + lo, a);
-    load_vec<T, V>(row + hi, b);
+  for (int i = 0; i < V; ++i) {
+    f[i] = a[i];
+    f[V + i] = b[i];
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a[i] = f[2 * i];
+    b[i] = f[2 * i + 1];
+  }
+}
+template <typename T, int V, int PAIRS>
+__device__ __forceinline__ void unpack_pairs(const RawPairs<T, V>& r, float (&a)[V], float (&b)[V]) {
+  unpack<T, V>(r.a, a);
+  unpack<T, V>(r.b, b);
+  if constexpr (V > 1 && PAIRS == PAIRS_INTERLEAVED) deal(a, b);
 }
 
 template <typename T, int V, int PAIRS>
-__device__ __forceinline__ void store_pairs(T* row, int p, int rot, int h, const float (&a)[V],
+__device__ __forceinline__ void store_pairs(T* row, int lo, int hi, bool on_hi, const float (&a)[V],
                                             const float (&b)[V]) {
-  int lo, hi;
-  pair_at<PAIRS>(p, rot, h, lo, hi);
-  if constexpr (V == 1) {
-    row[lo] = from_f32<T>(a[0]);
-    if (hi < h) row[hi] = from_f32<T>(b[0]);
-  } else if constexpr (PAIRS == PAIRS_INTERLEAVED) {
+  if constexpr (V > 1 && PAIRS == PAIRS_INTERLEAVED) {
     float f[2][V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -79,10 +85,10 @@ __device__ __forceinline__ void store_pairs(T* row, int p, int rot, int h, const
       f[(2 * i + 1) / V][(2 * i + 1) % V] = b[i];
     }
     store_vec<T, V>(row + lo, f[0]);
-    store_vec<T, V>(row + lo + V, f[1]);
+    store_vec<T, V>(row + hi, f[1]);
   } else {
     store_vec<T, V>(row + lo, a);
-    store_vec<T, V>(row + hi, b);
+    if (on_hi) store_vec<T, V>(row + hi, b);
   }
 }
 
@@ -91,187 +97,269 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// One tile of `tile` tokens (all heads) per iteration; E runs of V pairs per lane, `lanes`
-// lanes per row. Dynamic shared memory: float2[tile][rot / 2], and in the backward with
-// weights float[2][h] behind it.
-template <typename T, int V, int PAIRS, int E, bool BWD>
-__global__ void __launch_bounds__(kHeadThreads) head_kernel(HeadArgs a, int tile, int lanes) {
-  extern __shared__ float2 turns[];
-  const long long M = (long long)a.B * a.N;
-  const int half = a.rot / 2, npairs = (a.h + 1) / 2;
-  const int heads = a.H[0] + a.H[1] + a.H[2];
-  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes, groups = kHeadThreads / lanes;
-  float dw[2][E][2][V];
-  if (BWD) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-#pragma unroll
-        for (int q = 0; q < V; ++q) dw[i][e][0][q] = dw[i][e][1][q] = 0.0f;
-  }
-  for (long long m0 = (long long)blockIdx.x * tile; m0 < M; m0 += (long long)gridDim.x * tile) {
-    if (half) {
-      __syncthreads();   // the tile before is done with the angles
-      for (int i = threadIdx.x; i < tile * half; i += kHeadThreads) {
-        const long long m = m0 + i / half;
-        if (m >= M) break;
-        const double pos = a.positions ? (double)a.positions[m] : (double)(a.pos0 + m % a.N);
-        double turn = pos * (double)a.inv_freq[i % half] * kInvTwoPi;
-        turn -= rint(turn);
-        float2 cs;
-        sincospif((float)(2.0 * turn), &cs.y, &cs.x);
-        turns[i] = cs;
-      }
-      __syncthreads();
+// A walk over the rows of a group's token: the heads of q, then of k, then of v, in batches of R
+// rows `step` heads apart. All groups of a block walk alike (head - first is the same), whether
+// or not their token and head exist.
+template <typename T, int R>
+struct Walk {
+  int kind = 0, head = 0;
+  T* p[2];          // this head's row in one or two tensors
+  // On to the first head of the next tensor that has any; start(kind, which) gives its row.
+  template <typename F>
+  __device__ __forceinline__ void enter(const HeadArgs& a, int k, int first, F&& start) {
+    while (k < 3 && a.H[k] == 0) ++k;
+    kind = k;
+    head = first;
+    if (k < 3) {
+      p[0] = start(k, 0);
+      p[1] = start(k, 1);
     }
-    // Row i of the tile is token i % tile of head i / tile: neighbouring groups write
-    // neighbouring rows of the head-major output. All lanes of a warp take every iteration.
-    const int rows = tile * heads;
-    for (int i0 = 0; i0 < rows; i0 += groups) {
-      const int i = i0 + group;
-      const long long m = m0 + i % tile;
-      int head = i / tile;
-      const bool live = i < rows && m < M;
-      const int kind = head < a.H[0] ? 0 : head < a.H[0] + a.H[1] ? 1 : 2;
-      head -= kind == 0 ? 0 : kind == 1 ? a.H[0] : a.H[0] + a.H[1];
-      const long long b = m / a.N, t = m - b * a.N;
-      const T* x = static_cast<const T*>(a.x[kind]) + m * a.row[kind] + (long long)head * a.h;
-      const long long at = ((b * a.H[kind] + head) * a.N + t) * a.h;
-      const float2* cs = turns + (i % tile) * half;
-      const float* w = kind < 2 ? a.w[kind] : nullptr;
-      const bool normed = kind < 2 && a.norm != TTT_NORM_NONE;
-      const bool turned = kind < 2;
-      float xa[E][V], xb[E][V], ga[E][V], gb[E][V], wa[E][V], wb[E][V];
-      float ss = 0.0f, dot = 0.0f;
+  }
+  template <typename F>
+  __device__ __forceinline__ void next(const HeadArgs& a, int first, int step, long long s0, long long s1, F&& start) {
+    head += R * step;
+    p[0] += R * s0;
+    p[1] += R * s1;
+    if (head - first >= a.H[kind]) enter(a, kind + 1, first, start);
+  }
+};
+
+// A tile is 2^log_tile tokens: group g takes token g % tile and every (groups / tile)-th head of
+// it, so that a lane takes the angles of its pairs once for all heads, into registers, and
+// neighbouring groups write neighbouring rows of the head-major output. E runs of V pairs per
+// lane, `lanes` lanes per row. The next batch of rows is loaded before the current one is used,
+// and the first before the angles are taken. Dynamic shared memory in the backward with
+// weights: float[2][h].
+template <typename T, int V, int PAIRS, int E, bool BWD>
+__global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks : kFwdBlocks) : 1)
+    head_kernel(HeadArgs a, int log_tile, int lanes) {
+  extern __shared__ float acc[];
+  constexpr int R = BWD || E > 2 ? 1 : 2;   // rows of a batch
+  const int M = a.B * a.N, half = a.rot / 2, npairs = (a.h + 1) / 2;
+  const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
+  const int first = group >> log_tile, step = (kHeadThreads / lanes) >> log_tile;
+  const long long minor_step = (long long)step * a.h, major_step = minor_step * a.N;   // to the next head
+  const float inv_h = a.norm == TTT_NORM_RMS ? 1.0f / a.h : 1.0f;
+  int lo[E], hi[E];
+  bool on[E], on_hi[E];
+  float dw[2][E][2][V];
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int p = (e * lanes + lane) * V;
-        const bool on = live && p < npairs;
+  for (int e = 0; e < E; ++e) {
+    const int p = (e * lanes + lane) * V;
+    pair_at<PAIRS>(p, a.rot, a.h, lo[e], hi[e]);
+    on[e] = p < npairs;
+    on_hi[e] = on[e] && (V > 1 || hi[e] < a.h);
+    if (V > 1 && PAIRS == PAIRS_INTERLEAVED) hi[e] = lo[e] + V;   // two accesses of V elements
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-          xa[e][q] = xb[e][q] = ga[e][q] = gb[e][q] = 0.0f;
-          wa[e][q] = wb[e][q] = 1.0f;
+    for (int q = 0; q < V; ++q) dw[0][e][0][q] = dw[0][e][1][q] = dw[1][e][0][q] = dw[1][e][1][q] = 0.0f;
+  }
+
+  for (long long tile0 = (long long)blockIdx.x << log_tile; tile0 < M; tile0 += (long long)gridDim.x << log_tile) {
+    const long long m = tile0 + (group & ((1 << log_tile) - 1));
+    const bool live = m < M;
+    const int seq = live ? (int)m / a.N : 0, t = live ? (int)m - seq * a.N : 0;
+    const auto major_row = [&](int k) { return (((long long)seq * a.H[k] + first) * a.N + t) * a.h; };
+    const auto source = [&](int k, int which) {   // x, and in the backward dout
+      return which ? static_cast<const T*>(a.dout[k]) + major_row(k)
+                   : static_cast<const T*>(a.x[k]) + m * a.row[k] + first * a.h;
+    };
+    const auto target = [&](int k, int) {
+      return BWD ? static_cast<T*>(a.dx[k]) + (m * a.H[k] + first) * a.h : static_cast<T*>(a.out[k]) + major_row(k);
+    };
+    Walk<const T, R> in;
+    Walk<T, R> out;
+    in.enter(a, 0, first, source);
+    out.enter(a, 0, first, target);
+    RawPairs<T, V> rx[R][E], rg[BWD ? R : 1][E];
+    const auto fetch = [&]() {
+      const bool any = in.kind < 3 && live;
+      const int H = in.kind < 3 ? a.H[in.kind] : 0;
+#pragma unroll
+      for (int z = 0; z < R; ++z) {
+        const bool row = any && in.head + z * step < H;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const bool x = row && (!BWD || in.kind < 2);
+          load_raw_pairs<T, V>(rx[z][e], in.p[0] + z * minor_step, lo[e], hi[e], x && on[e], x && on_hi[e]);
+          if (BWD) load_raw_pairs<T, V>(rg[z][e], in.p[1] + z * major_step, lo[e], hi[e], row && on[e], row && on_hi[e]);
         }
-        if (!on) continue;
-        if (!BWD || turned) load_pairs<T, V, PAIRS>(x, p, a.rot, a.h, xa[e], xb[e]);
-        if (w) load_pairs<float, V, PAIRS>(w, p, a.rot, a.h, wa[e], wb[e]);
-        if (BWD) load_pairs<T, V, PAIRS>(static_cast<const T*>(a.dout[kind]) + at, p, a.rot, a.h, ga[e], gb[e]);
+      }
+      if (in.kind < 3) in.next(a, first, step, minor_step, BWD ? major_step : 0, source);
+    };
+    fetch();
+    float cs[E][V], sn[E][V], wa[E][V], wb[E][V];
+    const double pos = !live ? 0.0 : a.positions ? (double)a.positions[m] : (double)(a.pos0 + t);
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-          ss = fmaf(xa[e][q], xa[e][q], ss);
-          ss = fmaf(xb[e][q], xb[e][q], ss);
-          if (BWD && turned) {
-            if (p + q < half) {   // the rotation's transpose
-              const float2 c = cs[p + q];
-              const float u = ga[e][q], v = gb[e][q];
-              ga[e][q] = u * c.x + v * c.y;
-              gb[e][q] = v * c.x - u * c.y;
-            }
-            dot = fmaf(ga[e][q] * wa[e][q], xa[e][q], dot);
-            dot = fmaf(gb[e][q] * wb[e][q], xb[e][q], dot);
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const int p = (e * lanes + lane) * V + q;
+        cs[e][q] = 1.0f;   // behind the rotated elements: as they are
+        sn[e][q] = 0.0f;
+        if (p < half) {
+          double turn = pos * (double)a.inv_freq[p] * kInvTwoPi;
+          turn -= rint(turn);
+          sincospif((float)(2.0 * turn), &sn[e][q], &cs[e][q]);
+        }
+      }
+    int kind = -1;
+    while (out.kind < 3) {
+      float xa[R][E][V], xb[R][E][V], ga[R][E][V], gb[R][E][V];
+#pragma unroll
+      for (int z = 0; z < R; ++z)
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          unpack_pairs<T, V, PAIRS>(rx[z][e], xa[z][e], xb[z][e]);
+          if (BWD) unpack_pairs<T, V, PAIRS>(rg[z][e], ga[z][e], gb[z][e]);
+        }
+      fetch();
+      const int H = a.H[out.kind];
+      const auto write = [&](int z, int e, const float (&u)[V], const float (&v)[V]) {
+        if (live && out.head + z * step < H && on[e])
+          store_pairs<T, V, PAIRS>(out.p[0] + z * (BWD ? minor_step : major_step), lo[e], hi[e], on_hi[e], u, v);
+      };
+      if (out.kind == 2) {              // v is only laid out
+#pragma unroll
+        for (int z = 0; z < R; ++z)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            if constexpr (BWD) write(z, e, ga[z][e], gb[z][e]);
+            else write(z, e, xa[z][e], xb[z][e]);
+          }
+        out.next(a, first, step, BWD ? minor_step : major_step, 0, target);
+        continue;
+      }
+      if (out.kind != kind) {           // the first rows of q or k
+        kind = out.kind;
+        const float* w = a.w[kind];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+#pragma unroll
+          for (int q = 0; q < V; ++q) wa[e][q] = wb[e][q] = 1.0f;
+          if (w && on[e]) load_input<float, V>(w + lo[e], wa[e]);
+          if (w && on_hi[e]) load_input<float, V>(w + hi[e], wb[e]);
+          if constexpr (V > 1 && PAIRS == PAIRS_INTERLEAVED) deal(wa[e], wb[e]);
+        }
+      }
+#pragma unroll
+      for (int z = 0; z < R; ++z) {
+        float r = 1.0f, back = 0.0f, ss[V] = {}, dot[V] = {};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          fma_v<V>(ss, xa[z][e], xa[z][e], ss);
+          fma_v<V>(ss, xb[z][e], xb[z][e], ss);
+          if (BWD) {   // the rotation's transpose
+            float u[V], v[V], ns[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) ns[q] = -sn[e][q];
+            mul_v<V>(u, ga[z][e], ns);
+            mul_v<V>(v, gb[z][e], sn[e]);
+            fma_v<V>(ga[z][e], ga[z][e], cs[e], v);
+            fma_v<V>(gb[z][e], gb[z][e], cs[e], u);
+            mul_v<V>(u, ga[z][e], wa[e]);
+            mul_v<V>(v, gb[z][e], wb[e]);
+            fma_v<V>(dot, u, xa[z][e], dot);
+            fma_v<V>(dot, v, xb[z][e], dot);
           }
         }
-      }
-      const float inv_h = a.norm == TTT_NORM_RMS ? 1.0f / a.h : 1.0f;
-      ss = group_sum(ss, lanes);
-      const float r = normed ? rsqrtf(fmaf(ss, inv_h, a.eps)) : 1.0f;
-      float back = 0.0f;
-      if (BWD) {
-        dot = group_sum(dot, lanes);
-        back = normed ? r * r * r * dot * inv_h : 0.0f;
-      }
+        if (a.norm != TTT_NORM_NONE) {
+          float s = 0.0f, d = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int p = (e * lanes + lane) * V;
-        if (!live || p >= npairs) continue;
-        float oa[V], ob[V];
+          for (int q = 0; q < V; ++q) {
+            s += ss[q];
+            d += dot[q];
+          }
+          r = rsqrtf(fmaf(group_sum(s, lanes), inv_h, a.eps));
+          if (BWD) back = -r * r * r * group_sum(d, lanes) * inv_h;
+        }
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-          if (!BWD) {
-            const float u = xa[e][q] * r * wa[e][q], v = xb[e][q] * r * wb[e][q];
-            if (turned && p + q < half) {
-              const float2 c = cs[p + q];
-              oa[q] = u * c.x - v * c.y;
-              ob[q] = v * c.x + u * c.y;
-            } else {
-              oa[q] = u;
-              ob[q] = v;
-            }
+        for (int e = 0; e < E; ++e) {
+          float oa[V], ob[V], u[V], v[V];
+          if constexpr (!BWD) {
+            float ns[V];
+#pragma unroll
+            for (int q = 0; q < V; ++q) ns[q] = -sn[e][q];
+            mul_v<V>(u, xa[z][e], r);
+            mul_v<V>(v, xb[z][e], r);
+            mul_v<V>(u, u, wa[e]);
+            mul_v<V>(v, v, wb[e]);
+            mul_v<V>(oa, v, ns);
+            mul_v<V>(ob, u, sn[e]);
+            fma_v<V>(oa, u, cs[e], oa);
+            fma_v<V>(ob, v, cs[e], ob);
           } else {
-            oa[q] = fmaf(ga[e][q] * wa[e][q], r, -xa[e][q] * back);
-            ob[q] = fmaf(gb[e][q] * wb[e][q], r, -xb[e][q] * back);
-            if (w) {
-#pragma unroll
-              for (int z = 0; z < 2; ++z)
-                if (kind == z) {
-                  dw[z][e][0][q] = fmaf(ga[e][q] * r, xa[e][q], dw[z][e][0][q]);
-                  dw[z][e][1][q] = fmaf(gb[e][q] * r, xb[e][q], dw[z][e][1][q]);
-                }
+            // dx = r (g w) - x r^3 <g w, x> [/ h];  dw += g (x r)
+            mul_v<V>(oa, xa[z][e], back);
+            mul_v<V>(ob, xb[z][e], back);
+            mul_v<V>(u, ga[z][e], wa[e]);
+            mul_v<V>(v, gb[z][e], wb[e]);
+            fma_v<V>(oa, u, r, oa);
+            fma_v<V>(ob, v, r, ob);
+            if (a.partials) {
+              mul_v<V>(u, xa[z][e], r);
+              mul_v<V>(v, xb[z][e], r);
+              if (kind == 0) {
+                fma_v<V>(dw[0][e][0], ga[z][e], u, dw[0][e][0]);
+                fma_v<V>(dw[0][e][1], gb[z][e], v, dw[0][e][1]);
+              } else {
+                fma_v<V>(dw[1][e][0], ga[z][e], u, dw[1][e][0]);
+                fma_v<V>(dw[1][e][1], gb[z][e], v, dw[1][e][1]);
+              }
             }
           }
+          write(z, e, oa, ob);
         }
-        T* out = BWD ? static_cast<T*>(a.dx[kind]) + (m * a.H[kind] + head) * a.h
-                     : static_cast<T*>(a.out[kind]) + at;
-        store_pairs<T, V, PAIRS>(out, p, a.rot, a.h, oa, ob);
       }
+      out.next(a, first, step, BWD ? minor_step : major_step, 0, target);
     }
   }
   if (BWD && a.partials) {
     // one row of partial weight gradients per block: groups of a warp by shuffles, warps in
     // order through shared memory
-    float* acc = reinterpret_cast<float*>(turns + tile * half);
     for (int i = threadIdx.x; i < 2 * a.h; i += kHeadThreads) acc[i] = 0.0f;
-    __syncthreads();
+#pragma unroll
+    for (int z = 0; z < 2; ++z)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int q = 0; q < V; ++q)
+            for (int w = lanes; w < 32; w *= 2) dw[z][e][k][q] += __shfl_xor_sync(0xffffffffu, dw[z][e][k][q], w);
     for (int wp = 0; wp < kHeadThreads / 32; ++wp) {
+      __syncthreads();
+      if (threadIdx.x / 32 != wp || threadIdx.x % 32 >= lanes) continue;
 #pragma unroll
       for (int z = 0; z < 2; ++z)
 #pragma unroll
         for (int e = 0; e < E; ++e)
 #pragma unroll
           for (int q = 0; q < V; ++q) {
-            float u = dw[z][e][0][q], v = dw[z][e][1][q];
-            if (threadIdx.x / 32 != wp) continue;
-            for (int m = lanes; m < 32; m *= 2) {
-              u += __shfl_xor_sync(0xffffffffu, u, m);
-              v += __shfl_xor_sync(0xffffffffu, v, m);
-            }
             const int p = (e * lanes + lane) * V + q;
-            if (threadIdx.x % 32 >= lanes || p >= npairs) continue;
+            if (p >= npairs) continue;
             int lo, hi;
             pair_at<PAIRS>(p, a.rot, a.h, lo, hi);
-            acc[z * a.h + lo] += u;
-            if (hi < a.h) acc[z * a.h + hi] += v;
+            acc[z * a.h + lo] += dw[z][e][0][q];
+            if (hi < a.h) acc[z * a.h + hi] += dw[z][e][1][q];
           }
-      __syncthreads();
     }
+    __syncthreads();
     float* part = a.partials + (long long)blockIdx.x * 2 * a.h;
     for (int i = threadIdx.x; i < 2 * a.h; i += kHeadThreads) part[i] = acc[i];
   }
 }
 
-// Tokens of a tile: enough rows for two rounds of the block's groups, while the tiles still
-// give every SM four blocks.
-int head_tile(const HeadArgs& a, int groups) {
-  const long long M = (long long)a.B * a.N;
-  const int heads = a.H[0] + a.H[1] + a.H[2];
-  int tile = 1;
-  while (tile < kMaxTile && tile * heads < 2 * groups && M / (2 * tile) >= 148 * 4) tile *= 2;
-  return tile;
-}
-
 template <typename T, int V, int PAIRS, int E, bool BWD>
 cudaError_t launch_tiles(const HeadArgs& a, int lanes, cudaStream_t s) {
-  const int tile = head_tile(a, kHeadThreads / lanes);
-  const long long M = (long long)a.B * a.N, tiles = (M + tile - 1) / tile;
-  // at most 32 KB of angles: a row of 256 pairs takes 32 lanes, which makes 16 tokens
-  size_t smem = (size_t)tile * (a.rot / 2) * sizeof(float2);
-  long long blocks = tiles;
-  if (BWD) {
-    blocks = head_bwd_blocks(a.B, a.N);
-    if (a.partials) smem += 2 * (size_t)a.h * sizeof(float);
-  }
-  head_kernel<T, V, PAIRS, E, BWD><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, tile, lanes);
+  // A token per group, while the tiles still give every SM four blocks.
+  const long long M = (long long)a.B * a.N;
+  const int groups = kHeadThreads / lanes;
+  int log_tile = 0;
+  while (2 << log_tile <= groups && (M >> (log_tile + 1)) >= 148 * 4) ++log_tile;
+  const long long tiles = (M + (1 << log_tile) - 1) >> log_tile;
+  const long long blocks = BWD ? head_bwd_blocks(a.B, a.N) : tiles;
+  const size_t smem = BWD && a.partials ? 2 * (size_t)a.h * sizeof(float) : 0;
+  head_kernel<T, V, PAIRS, E, BWD><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, log_tile, lanes);
   return cudaGetLastError();
 }
 
@@ -329,7 +417,7 @@ cudaError_t launch(int dt, const HeadArgs& a, cudaStream_t s) {
 
 long long head_bwd_blocks(int B, int N) {
   const long long M = (long long)B * N;
-  return M < 148 * 4 ? M : 148 * 4;
+  return M < 148 * kBwdBlocks ? M : 148 * kBwdBlocks;   // one wave
 }
 
 cudaError_t head_fwd(int dt, const HeadArgs& a, cudaStream_t s) { return launch<false>(dt, a, s); }

@@ -8,6 +8,67 @@ namespace ttt {
 
 using bf16 = __nv_bfloat16;
 
+// Two-wide fp32: one issue slot for two operations.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
+
+// o = a * b (+ c) for V values, pairwise.
+template <int V>
+__device__ __forceinline__ void mul_v(float (&o)[V], const float (&a)[V], const float (&b)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if constexpr (V == 1) o[0] = a[0] * b[0];
+    else unpack2(mul2(pack2(a[i], a[i + 1]), pack2(b[i], b[i + 1])), o[i], o[i + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void mul_v(float (&o)[V], const float (&a)[V], float b) {
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if constexpr (V == 1) o[0] = a[0] * b;
+    else unpack2(mul2(pack2(a[i], a[i + 1]), both(b)), o[i], o[i + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void fma_v(float (&o)[V], const float (&a)[V], const float (&b)[V], const float (&c)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if constexpr (V == 1) o[0] = fmaf(a[0], b[0], c[0]);
+    else unpack2(fma2(pack2(a[i], a[i + 1]), pack2(b[i], b[i + 1]), pack2(c[i], c[i + 1])), o[i], o[i + 1]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void fma_v(float (&o)[V], const float (&a)[V], float b, const float (&c)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if constexpr (V == 1) o[0] = fmaf(a[0], b, c[0]);
+    else unpack2(fma2(pack2(a[i], a[i + 1]), both(b), pack2(c[i], c[i + 1])), o[i], o[i + 1]);
+  }
+}
+
 // V consecutive elements in one access (V * sizeof(T) in {2, 4, 8, 16} bytes and aligned to
 // that).
 template <typename T, int V> struct Pack;
@@ -96,6 +157,29 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) x.t[i] = from_f32<T>(f[i]);
     *reinterpret_cast<typename Pack<T, V>::U*>(p) = x.u;
+  }
+}
+
+// V elements of an input that nothing writes while the kernel runs (the read-only path: later
+// loads may pass earlier stores).
+__device__ __forceinline__ unsigned short ldg(const unsigned short* p) { return __ldg(p); }
+__device__ __forceinline__ unsigned ldg(const unsigned* p) { return __ldg(p); }
+__device__ __forceinline__ uint2 ldg(const uint2* p) { return __ldg(p); }
+__device__ __forceinline__ uint4 ldg(const uint4* p) { return __ldg(p); }
+
+template <typename T, int V>
+__device__ __forceinline__ void load_input(const T* p, float (&f)[V]) {
+  if constexpr (V * sizeof(T) > 16) {
+    float lo[V / 2], hi[V / 2];
+    load_input<T, V / 2>(p, lo);
+    load_input<T, V / 2>(p + V / 2, hi);
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      f[i] = lo[i];
+      f[V / 2 + i] = hi[i];
+    }
+  } else {
+    unpack<T, V>(ldg(reinterpret_cast<const typename Pack<T, V>::U*>(p)), f);
   }
 }
 

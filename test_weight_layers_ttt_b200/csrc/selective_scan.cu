@@ -29,31 +29,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// ---------------------------------------------------------------- two-wide fp32
-using f2 = unsigned long long;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-  f2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+// ---------------------------------------------------------------- exponentials
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -69,7 +45,6 @@ __device__ __forceinline__ f2 ex2_2(f2 v) {
 // a polynomial of degree 9, interpolated at the Chebyshev nodes of [0, 1] (relative error 1.2e-7
 // in fp32): it keeps the relative accuracy of small steps, which a logarithm of 1 + e loses, and
 // leaves the exponential unit alone.
-__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
 __device__ __forceinline__ f2 softplus2(f2 x) {
   float lo, hi;
   unpack2(x, lo, hi);
@@ -370,22 +345,41 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs a, int SP) {
     const bool on = s < a.S;
     const float A2 = on ? a.A[(long long)d * a.S + s] * kLog2e : 0.0f;
     const long long io = bd * a.S + s;
+    // four chunks' loads at a time: the recurrence itself is short, its loads are not
+    const long long bk = (long long)b * a.chunks;
+    const auto entry = [&](int k) { return ((bk + k) * a.D + d) * SP + s; };
     float h = on && a.state_in ? a.state_in[io] : 0.0f;
-    for (int k = 0; k < a.chunks; ++k) {
-      const long long bk = (long long)b * a.chunks + k, at = (bk * a.D + d) * SP + s;
-      const float end = k + 1 < a.chunks ? a.ends[at] : 0.0f;
-      const float e = k + 1 < a.chunks ? ex2(A2 * a.dsum[bk * a.D + d]) : 0.0f;
-      a.ends[at] = h;
-      h = fmaf(e, h, end);
+    for (int k0 = 0; k0 < a.chunks; k0 += 4) {
+      float end[4], sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = k0 + j + 1 < a.chunks;   // the last chunk's end is nobody's start
+        end[j] = in ? a.ends[entry(k0 + j)] : 0.0f;
+        sum[j] = in ? a.dsum[(bk + k0 + j) * a.D + d] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (k0 + j >= a.chunks) break;
+        a.ends[entry(k0 + j)] = h;
+        h = fmaf(ex2(A2 * sum[j]), h, end[j]);
+      }
     }
     if (!BWD) continue;
     float g = on && a.dstate_out ? a.dstate_out[io] : 0.0f;
-    for (int k = a.chunks - 1; k >= 0; --k) {
-      const long long bk = (long long)b * a.chunks + k, at = (bk * a.D + d) * SP + s;
-      const float share = k > 0 ? a.back[at] : 0.0f;
-      const float e = k > 0 ? ex2(A2 * a.dsum[bk * a.D + d]) : 0.0f;
-      a.back[at] = g;
-      g = fmaf(e, g, share);
+    for (int k0 = a.chunks - 1; k0 >= 0; k0 -= 4) {
+      float share[4], sum[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = k0 - j > 0;
+        share[j] = in ? a.back[entry(k0 - j)] : 0.0f;
+        sum[j] = in ? a.dsum[(bk + k0 - j) * a.D + d] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (k0 - j < 0) break;
+        a.back[entry(k0 - j)] = g;
+        g = fmaf(ex2(A2 * sum[j]), g, share[j]);
+      }
     }
   }
 }
@@ -1125,7 +1119,7 @@ int scan_channel_blocks(int D, int G, int S) {
 // Blocks that run at a time (148 SMs x 7 forward, x 3 backward), and the tokens' worth of work
 // that starting and joining a chunk costs. The forward's first pass doubles its exponentials,
 // so a sequence is cut for it only where whole sequences would leave most SMs idle.
-constexpr long long kFwdSlots = 148 * 7, kBwdSlots = 148 * 3, kChunkCost = 64;
+constexpr long long kFwdSlots = 148 * 7, kBwdSlots = 148 * 3, kChunkCost = 24;
 
 int scan_chunks(int B, int N, int D, int G, int S, bool backward, int* chunk) {
   const int CB = backward ? kWarps * 64 / state_lanes(S) : kFwdWarps * 32 / state_lanes(S);
