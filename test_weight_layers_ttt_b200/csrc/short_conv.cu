@@ -5,7 +5,7 @@
 // write backward. A thread owns V consecutive channels over a run of tokens and slides the
 // window through registers, so a row is read once per run (plus width - 1 halo rows) and every
 // access of the vector form is 8 or 16 bytes. The next kAhead rows are loaded before the
-// current ones are used: bytes in flight, not arithmetic, set the rate.
+// current ones are used: bytes in flight set the rate, and the arithmetic is two-wide.
 #include "mixer.h"
 #include "mixer_common.cuh"
 
@@ -13,7 +13,7 @@ namespace ttt {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kAhead = 4;    // rows loaded together
+constexpr int kAhead = 4;    // rows loaded together, while the rows before are used
 
 __device__ __forceinline__ int sequence_length(const int* lens, int b, int N) {
   return lens ? min(max(lens[b], 0), N) : N;
@@ -63,24 +63,29 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int 
 #pragma unroll
     for (int j = 1; j < K; ++j) history_row<T, V, K>(a, b, c, (long long)t0 - j + K - 1, win[j - 1]);
     const int te = min(t1, n);
+    typename Pack<T, V>::U next[kAhead];
+    const auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load_here(x + (long long)(t + i) * a.x_row, t + i < te, next[i]);
+    };
+    fetch(t0);
     for (int t = t0; t < te; t += kAhead) {
       typename Pack<T, V>::U raw[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (t + i < te) raw[i] = load_raw<T, V>(x + (long long)(t + i) * a.x_row);
+      for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
+      fetch(t + kAhead);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        if (t + i >= te) break;
         float cur[V], o[V];
         unpack<T, V>(raw[i], cur);
+        fma_v<V>(o, w[0], cur, bias);
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-          float acc = fmaf(w[0][q], cur[q], bias[q]);
+        for (int j = 1; j < K; ++j) fma_v<V>(o, w[j], win[j - 1], o);
+        if (a.act) {
 #pragma unroll
-          for (int j = 1; j < K; ++j) acc = fmaf(w[j][q], win[j - 1][q], acc);
-          o[q] = a.act ? acc * fast_sigmoid(acc) : acc;
+          for (int q = 0; q < V; ++q) o[q] *= fast_sigmoid(o[q]);
         }
-        store_vec<T, V>(y + (long long)(t + i) * a.D, o);
+        if (t + i < te) store_vec<T, V>(y + (long long)(t + i) * a.D, o);
 #pragma unroll
         for (int q = 0; q < V; ++q) {
 #pragma unroll
@@ -177,49 +182,51 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
 #pragma unroll
       for (int q = 0; q < V; ++q) win[j - 1][q] = 0.0f;
   }
-  const int s1 = t1 + K - 1;
+  const int s1 = t1 + K - 1, se = min(s1, n);
+  typename Pack<T, V>::U nx[kAhead], ng[kAhead];
+  const auto fetch = [&](int s) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      load_here(x + (long long)(s + i) * a.x_row, s + i < se, nx[i]);
+      load_here(dy + (long long)(s + i) * a.D, s + i < se, ng[i]);
+    }
+  };
+  fetch(t0);
   for (int s0 = t0; s0 < s1; s0 += kAhead) {
     typename Pack<T, V>::U rx[kAhead], rg[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (s0 + i < min(s1, n)) {
-        rx[i] = load_raw<T, V>(x + (long long)(s0 + i) * a.x_row);
-        rg[i] = load_raw<T, V>(dy + (long long)(s0 + i) * a.D);
-      }
+    for (int i = 0; i < kAhead; ++i) {
+      rx[i] = nx[i];
+      rg[i] = ng[i];
+    }
+    fetch(s0 + kAhead);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int s = s0 + i;
-      if (s >= s1) break;
       float cur[V];
 #pragma unroll
-      for (int q = 0; q < V; ++q) {
+      for (int q = 0; q < V; ++q)
 #pragma unroll
         for (int j = K - 1; j > 0; --j) g[j][q] = g[j - 1][q];
-        g[0][q] = 0.0f;
-        cur[q] = 0.0f;
+      unpack<T, V>(rx[i], cur);       // zeros behind the sequence's end
+      unpack<T, V>(rg[i], g[0]);
+      if (a.act) {
+        float pre[V];
+        fma_v<V>(pre, w[0], cur, bias);
+#pragma unroll
+        for (int j = 1; j < K; ++j) fma_v<V>(pre, w[j], win[j - 1], pre);
+#pragma unroll
+        for (int q = 0; q < V; ++q) {
+          const float sg = fast_sigmoid(pre[q]);
+          g[0][q] *= sg * fmaf(pre[q], 1.0f - sg, 1.0f);
+        }
       }
-      if (s < n) {
-        unpack<T, V>(rx[i], cur);
-        unpack<T, V>(rg[i], g[0]);
-        if (a.act) {
+      if (s < se && s < t1) {         // this run's own tokens
+        fma_v<V>(dw[0], g[0], cur, dw[0]);
 #pragma unroll
-          for (int q = 0; q < V; ++q) {
-            float pre = fmaf(w[0][q], cur[q], bias[q]);
+        for (int j = 1; j < K; ++j) fma_v<V>(dw[j], g[0], win[j - 1], dw[j]);
 #pragma unroll
-            for (int j = 1; j < K; ++j) pre = fmaf(w[j][q], win[j - 1][q], pre);
-            const float sg = fast_sigmoid(pre);
-            g[0][q] *= sg * fmaf(pre, 1.0f - sg, 1.0f);
-          }
-        }
-        if (s < t1) {
-#pragma unroll
-          for (int q = 0; q < V; ++q) {
-            dw[0][q] = fmaf(g[0][q], cur[q], dw[0][q]);
-#pragma unroll
-            for (int j = 1; j < K; ++j) dw[j][q] = fmaf(g[0][q], win[j - 1][q], dw[j][q]);
-            db[q] += g[0][q];
-          }
-        }
+        for (int q = 0; q < V; ++q) db[q] += g[0][q];
       }
 #pragma unroll
       for (int q = 0; q < V; ++q) {
@@ -227,15 +234,12 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
         for (int j = K - 2; j > 0; --j) win[j][q] = win[j - 1][q];
         win[0][q] = cur[q];
       }
-      const int t = s - (K - 1);   // the row of dx that g[s] completes
-      if (t >= t0 || r == 0) {
+      const int t = s - (K - 1);      // the row of dx that g[s] completes
+      if (s < s1 && (t >= t0 || r == 0)) {
         float o[V];
+        mul_v<V>(o, w[0], g[K - 1]);
 #pragma unroll
-        for (int q = 0; q < V; ++q) {
-          o[q] = w[0][q] * g[K - 1][q];
-#pragma unroll
-          for (int j = 1; j < K; ++j) o[q] = fmaf(w[j][q], g[K - 1 - j][q], o[q]);
-        }
+        for (int j = 1; j < K; ++j) fma_v<V>(o, w[j], g[K - 1 - j], o);
         const int i_out = t + K - 1 - n;   // the row of dstate_out that this row became
         if (a.dstate_out && i_out >= 0 && i_out < K - 1) {
           float f[V];
@@ -261,21 +265,22 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
   }
 }
 
-// 32 columns x 8 row groups per block; row group g adds rows g, g + 8, ... in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* part, long long R, long long C,
-                                                          float* out0, long long n0, float* out1) {
-  __shared__ float acc[8][33];
+// 32 columns x 16 row groups per block; row group g adds rows g, g + 16, ... in order.
+constexpr int kSumRows = 16;
+__global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const float* part, long long R, long long C,
+                                                                    float* out0, long long n0, float* out1) {
+  __shared__ float acc[kSumRows][33];
   const long long c = (long long)blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
   if (c < C) {
-#pragma unroll 4
-    for (long long r = threadIdx.y; r < R; r += 8) v += part[r * C + c];
+#pragma unroll 8
+    for (long long r = threadIdx.y; r < R; r += kSumRows) v += part[r * C + c];
   }
   acc[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y == 0 && c < C) {
 #pragma unroll
-    for (int g = 1; g < 8; ++g) v += acc[g][threadIdx.x];
+    for (int g = 1; g < kSumRows; ++g) v += acc[g][threadIdx.x];
     if (c < n0) {
       if (out0) out0[c] = v;
     } else if (out1) {
@@ -355,7 +360,7 @@ cudaError_t launch(int dt, const ConvArgs& a, cudaStream_t s) {
 
 cudaError_t column_sums(const float* part, long long R, long long C, float* out0, long long n0,
                         float* out1, cudaStream_t s) {
-  column_sums_kernel<<<(unsigned)((C + 31) / 32), dim3(32, 8), 0, s>>>(part, R, C, out0, n0, out1);
+  column_sums_kernel<<<(unsigned)((C + 31) / 32), dim3(32, kSumRows), 0, s>>>(part, R, C, out0, n0, out1);
   return cudaGetLastError();
 }
 

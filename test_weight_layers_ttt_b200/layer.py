@@ -11,6 +11,8 @@ they run on the device of their first tensor, on its current stream unless ``str
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import abi
@@ -257,19 +259,22 @@ NORMS = {None: abi.TTT_NORM_NONE, "rms": abi.TTT_NORM_RMS, "l2": abi.TTT_NORM_L2
 PAIRS = {"halves": abi.TTT_PAIRS_HALVES, "interleaved": abi.TTT_PAIRS_INTERLEAVED}
 
 
-class _On:
-    """The device of a call's tensors as the current one (a no-op when it already is)."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on_device(fn):
+    """Runs ``fn`` with the device of its first tensor as the current one, and on that device's
+    current stream when none is given."""
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        device = next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if device is None or device.type != "cuda":
+            return fn(*args, **kw)
+        index = device.index
+        if kw.get("stream") is None:
+            kw["stream"] = torch._C._cuda_getCurrentRawStream(index)
+        if index == torch._C._cuda_getDevice():
+            return fn(*args, **kw)
+        with torch.cuda.device(device):
+            return fn(*args, **kw)
+    return call
 
 
 def _choice(table, key, name):
@@ -280,7 +285,7 @@ def _choice(table, key, name):
 
 def _dense(t, name, shape, dtype, device):
     """A contiguous tensor of exactly this shape and type, or None."""
-    if t is None:
+    if t is None or t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
         return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -294,7 +299,7 @@ def _dense(t, name, shape, dtype, device):
 
 def _rows(t, name, lead, width, dtype, device):
     """Elements between the tokens of ``t`` [*lead, *width] (lead: B, N or B); 0 when None."""
-    if t is None:
+    if t is None or t.dtype is dtype and t.is_contiguous() and t.shape == lead + width and t.device == device:
         return 0
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -325,6 +330,15 @@ def _rows(t, name, lead, width, dtype, device):
     return row
 
 
+def _scratch(ws, nbytes, device):
+    """The caller's workspace, or a new one of ``nbytes`` (None when none is needed)."""
+    if ws is None:
+        return workspace(nbytes, device) if nbytes else None
+    if ws.device != device:
+        raise ValueError(f"ws must be on {device}, got {ws.device}")
+    return ws
+
+
 def _first(t, name, dims):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -347,6 +361,7 @@ def _conv_desc(x, w, bias, act, state, lens, lead):
                              _choice(ACTS, act, "act"), _rows(x, "x", lead, (D,), x.dtype, device))
 
 
+@_on_device
 def short_conv_fwd(x, w, *, bias=None, act="silu", state=None, lens=None, return_state=True,
                    out=None, state_out=None, stream=None):
     """Short causal depthwise convolution of x [B,N,D] with taps w [width,D] (tap j multiplies
@@ -357,30 +372,30 @@ def short_conv_fwd(x, w, *, bias=None, act="silu", state=None, lens=None, return
     desc = _conv_desc(x, w, bias, act, state, lens, tuple(x.shape[:2]))
     B, N, D = x.shape
     shape = (B, desc.width - 1, D)
-    with _On(device):
-        if out is None:
-            out = torch.empty((B, N, D), dtype=x.dtype, device=device)
-        _dense(out, "out", (B, N, D), x.dtype, device)
-        if state_out is None and return_state:
-            state_out = torch.empty(shape, dtype=x.dtype, device=device)
-        _dense(state_out, "state_out", shape, x.dtype, device)
-        abi.ttt_short_conv_fwd(desc, x, w, bias, state, lens, out, state_out, stream=stream)
+    if out is None:
+        out = torch.empty((B, N, D), dtype=x.dtype, device=device)
+    _dense(out, "out", (B, N, D), x.dtype, device)
+    if state_out is None and return_state:
+        state_out = torch.empty(shape, dtype=x.dtype, device=device)
+    _dense(state_out, "state_out", shape, x.dtype, device)
+    abi.ttt_short_conv_fwd(desc, x, w, bias, state, lens, out, state_out, stream=stream)
     return out, state_out
 
 
+@_on_device
 def short_conv_step(x, w, state, *, bias=None, act="silu", out=None, stream=None):
     """The next token x [B,D] of B sequences; ``state`` [B,width-1,D] is shifted in place.
     Returns y [B,D]."""
     device = _first(x, "x", 2)
     desc = _conv_desc(x, w, bias, act, state, None, (x.shape[0],))
-    with _On(device):
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        _dense(out, "out", x.shape, x.dtype, device)
-        abi.ttt_short_conv_step(desc, x, w, bias, state, out, stream=stream)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    _dense(out, "out", x.shape, x.dtype, device)
+    abi.ttt_short_conv_step(desc, x, w, bias, state, out, stream=stream)
     return out
 
 
+@_on_device
 def short_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lens=None, dstate=None,
                    ws=None, stream=None):
     """Backward of short_conv_fwd for dy [B,N,D] and ``dstate``, the gradient of the returned
@@ -391,15 +406,13 @@ def short_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lens=None, ds
     B, N, D = x.shape
     _dense(dy, "dy", (B, N, D), x.dtype, device)
     _dense(dstate, "dstate", (B, desc.width - 1, D), x.dtype, device)
-    with _On(device):
-        dx = torch.empty((B, N, D), dtype=x.dtype, device=device)
-        dw = torch.empty_like(w)
-        dbias = None if bias is None else torch.empty_like(bias)
-        dstate_in = None if state is None else torch.empty_like(state)
-        if ws is None:
-            ws = workspace(abi.ttt_short_conv_bwd_workspace_bytes(desc), device)
-        abi.ttt_short_conv_bwd(desc, x, w, bias, state, lens, dy, dstate, dx, dw, dbias, dstate_in,
-                               ws, stream=stream)
+    dx = torch.empty((B, N, D), dtype=x.dtype, device=device)
+    dw = torch.empty_like(w)
+    dbias = None if bias is None else torch.empty_like(bias)
+    dstate_in = None if state is None else torch.empty_like(state)
+    ws = _scratch(ws, abi.ttt_short_conv_bwd_workspace_bytes(desc), device)
+    abi.ttt_short_conv_bwd(desc, x, w, bias, state, lens, dy, dstate, dx, dw, dbias, dstate_in,
+                           ws, stream=stream)
     return dx, dw, dbias, dstate_in
 
 
@@ -428,6 +441,7 @@ def _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs):
                               eps, pos0, row[0], row[1], row[2]), some
 
 
+@_on_device
 def head_norm_rope_fwd(q, k, v=None, *, wq=None, wk=None, norm="l2", eps=1e-6, inv_freq=None,
                        positions=None, pos0=0, pairs="halves", stream=None):
     """The layer's q, k, v [B,H,N,h] from the projection's token-major q, k, v [B,N,H,h] (any
@@ -436,14 +450,14 @@ def head_norm_rope_fwd(q, k, v=None, *, wq=None, wk=None, norm="l2", eps=1e-6, i
     int32, or pos0 + t), and v laid out. Returns (q, k, v)."""
     desc, some = _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs)
     B, N, _, h = some.shape
-    with _On(some.device):
-        out = [None if t is None else
-               torch.empty((B, t.shape[2], N, h), dtype=t.dtype, device=some.device)
-               for t in (q, k, v)]
-        abi.ttt_head_norm_rope_fwd(desc, q, k, v, wq, wk, inv_freq, positions, *out, stream=stream)
+    out = [None if t is None else
+           torch.empty((B, t.shape[2], N, h), dtype=t.dtype, device=some.device)
+           for t in (q, k, v)]
+    abi.ttt_head_norm_rope_fwd(desc, q, k, v, wq, wk, inv_freq, positions, *out, stream=stream)
     return tuple(out)
 
 
+@_on_device
 def head_norm_rope_bwd(q, k, v, dq, dk, dv, *, wq=None, wk=None, norm="l2", eps=1e-6,
                        inv_freq=None, positions=None, pos0=0, pairs="halves", ws=None,
                        stream=None):
@@ -457,14 +471,13 @@ def head_norm_rope_bwd(q, k, v, dq, dk, dv, *, wq=None, wk=None, norm="l2", eps=
             raise ValueError(f"{name} must be given exactly when its tensor is")
         if g is not None:
             _dense(g, name, (B, t.shape[2], N, h), some.dtype, device)
-    with _On(device):
-        out = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
-               for t in (q, k, v)]
-        dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
-        if ws is None and (wq is not None or wk is not None):
-            ws = workspace(abi.ttt_head_norm_rope_bwd_workspace_bytes(desc), device)
-        abi.ttt_head_norm_rope_bwd(desc, q, k, wq, wk, inv_freq, positions, dq, dk, dv, *out, dwq,
-                                   dwk, ws, stream=stream)
+    out = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
+           for t in (q, k, v)]
+    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+    sums = wq is not None or wk is not None
+    ws = _scratch(ws, abi.ttt_head_norm_rope_bwd_workspace_bytes(desc) if sums else 0, device)
+    abi.ttt_head_norm_rope_bwd(desc, q, k, wq, wk, inv_freq, positions, dq, dk, dv, *out, dwq,
+                               dwk, ws, stream=stream)
     return (*out, dwq, dwk)
 
 
@@ -490,6 +503,7 @@ def _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, lens, lead):
                              _rows(Cm, "Cm", lead, (G, S), dtype, device))
 
 
+@_on_device
 def selective_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softplus=True,
                        state=None, lens=None, return_state=True, out=None, state_out=None, ws=None,
                        stream=None):
@@ -500,36 +514,34 @@ def selective_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softpl
     device = _first(u, "u", 3)
     desc = _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, lens, tuple(u.shape[:2]))
     shape = (desc.B, desc.D, desc.S)
-    with _On(device):
-        if out is None:
-            out = torch.empty(u.shape, dtype=u.dtype, device=device)
-        _dense(out, "out", u.shape, u.dtype, device)
-        if state_out is None and return_state:
-            state_out = torch.empty(shape, dtype=torch.float32, device=device)
-        _dense(state_out, "state_out", shape, torch.float32, device)
-        if ws is None:
-            need = abi.ttt_selective_scan_workspace_bytes(desc, 0)
-            ws = workspace(need, device) if need else None
-        abi.ttt_selective_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, out,
-                                   state_out, ws, stream=stream)
+    if out is None:
+        out = torch.empty(u.shape, dtype=u.dtype, device=device)
+    _dense(out, "out", u.shape, u.dtype, device)
+    if state_out is None and return_state:
+        state_out = torch.empty(shape, dtype=torch.float32, device=device)
+    _dense(state_out, "state_out", shape, torch.float32, device)
+    ws = _scratch(ws, abi.ttt_selective_scan_workspace_bytes(desc, 0), device)
+    abi.ttt_selective_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, out,
+                               state_out, ws, stream=stream)
     return out, state_out
 
 
+@_on_device
 def selective_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None, softplus=True,
                         out=None, stream=None):
     """The next token of B sequences: u, dt, z [B,D], Bm, Cm [B,G,S]; ``state`` [B,D,S] fp32 is
     updated in place. Returns y [B,D]."""
     device = _first(u, "u", 2)
     desc = _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, None, (u.shape[0],))
-    with _On(device):
-        if out is None:
-            out = torch.empty(u.shape, dtype=u.dtype, device=device)
-        _dense(out, "out", u.shape, u.dtype, device)
-        abi.ttt_selective_scan_step(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, out,
-                                    stream=stream)
+    if out is None:
+        out = torch.empty(u.shape, dtype=u.dtype, device=device)
+    _dense(out, "out", u.shape, u.dtype, device)
+    abi.ttt_selective_scan_step(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, out,
+                                stream=stream)
     return out
 
 
+@_on_device
 def selective_scan_bwd(u, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=None, softplus=True,
                        state=None, lens=None, dstate=None, ws=None, stream=None):
     """Backward of selective_scan_fwd for dy [B,N,D] and ``dstate``, the gradient of the
@@ -543,12 +555,10 @@ def selective_scan_bwd(u, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=None, so
     def new(t):
         return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
 
-    with _On(device):
-        du, ddt, dA, dB, dC = new(u), new(dt), new(A), new(Bm), new(Cm)
-        dD, dz, dbias, dstate_in = new(D), new(z), new(dt_bias), new(state)
-        if ws is None:
-            ws = workspace(abi.ttt_selective_scan_workspace_bytes(desc, 1), device)
-        abi.ttt_selective_scan_bwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, dy, dstate,
-                                   du, ddt, dA, dB, dC, dD, dz, dbias, dstate_in, ws,
-                                   stream=stream)
+    du, ddt, dA, dB, dC = new(u), new(dt), new(A), new(Bm), new(Cm)
+    dD, dz, dbias, dstate_in = new(D), new(z), new(dt_bias), new(state)
+    ws = _scratch(ws, abi.ttt_selective_scan_workspace_bytes(desc, 1), device)
+    abi.ttt_selective_scan_bwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, dy, dstate,
+                               du, ddt, dA, dB, dC, dD, dz, dbias, dstate_in, ws,
+                               stream=stream)
     return du, ddt, dA, dB, dC, dD, dz, dbias, dstate_in
