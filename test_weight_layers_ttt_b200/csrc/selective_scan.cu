@@ -783,13 +783,22 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
       h4[z][0] = h0[z][0] = fma2(ex2_2(mul2(m2, A2[z][0])), pack2(S4.x, S4.y), pack2(M4.x, M4.y));
       h4[z][1] = h0[z][1] = fma2(ex2_2(mul2(m2, A2[z][1])), pack2(S4.z, S4.w), pack2(M4.z, M4.w));
     }
-    // one token forward: its a_t, and the state behind it in place
-    const auto advance = [&](int k, f2 (&e)[2][2], f2 (&h)[2][2]) {
+    // Operands of a token, read one token ahead of their use.
+    struct Operands {
+      float4 du, B, C;
+      float2 g;
+    };
+    const auto read = [&](int k, Operands& o, bool with_c, bool with_g) {
       read_again();
-      const float4 du = sm.du[k * (CB / 2) + pair];
-      const float4 B4 = *reinterpret_cast<const float4*>(&sm.B[k * SP + sl * 4]);
-      const f2 B2[2] = {pack2(B4.x, B4.y), pack2(B4.z, B4.w)};
-      const f2 d2[2] = {both(du.x), both(du.y)}, x2[2] = {both(du.z), both(du.w)};
+      o.du = sm.du[k * (CB / 2) + pair];
+      o.B = *reinterpret_cast<const float4*>(&sm.B[k * SP + sl * 4]);
+      if (with_c) o.C = *reinterpret_cast<const float4*>(&sm.C[k * SP + sl * 4]);
+      if (with_g) o.g = *reinterpret_cast<const float2*>(&sm.g[k * CB + 2 * pair]);
+    };
+    // one token forward: its a_t, and the state behind it in place
+    const auto advance = [&](const Operands& o, f2 (&e)[2][2], f2 (&h)[2][2]) {
+      const f2 B2[2] = {pack2(o.B.x, o.B.y), pack2(o.B.z, o.B.w)};
+      const f2 d2[2] = {both(o.du.x), both(o.du.y)}, x2[2] = {both(o.du.z), both(o.du.w)};
 #pragma unroll
       for (int z = 0; z < 2; ++z)
 #pragma unroll
@@ -798,9 +807,8 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
           h[z][i] = fma2(e[z][i], h[z][i], mul2(x2[z], B2[i]));
         }
     };
-    const auto read_out = [&](int k, const f2 (&h)[2][2]) {
-      const float4 C4 = *reinterpret_cast<const float4*>(&sm.C[k * SP + sl * 4]);
-      const f2 C2[2] = {pack2(C4.x, C4.y), pack2(C4.z, C4.w)};
+    const auto read_out = [&](int k, const Operands& o, const f2 (&h)[2][2]) {
+      const f2 C2[2] = {pack2(o.C.x, o.C.y), pack2(o.C.z, o.C.w)};
       float y[2];
 #pragma unroll
       for (int z = 0; z < 2; ++z) {
@@ -810,12 +818,29 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
       }
       sm.y[k * kThreads + lane_sum] = make_float2(y[0], y[1]);
     };
+    // the sums over the warp's channels of token k: lane cl gets those from index cl * 8 / CL on
+    const auto sum_channels = [&](int k, float (&v)[8]) {
+      butterfly<CL, 0, 8>(v, lane);
+      constexpr int SHARE = CL > 8 ? CL / 8 : 1, OV = CL > 8 ? 1 : 8 / CL;
+      if (cl % SHARE == 0) {
+#pragma unroll
+        for (int q = 0; q < OV; ++q) {
+          const int id = cl / SHARE * OV + q;
+          sm.w[warp][k][(id / 4) * SP + sl * 4 + id % 4] = v[q];
+        }
+      }
+    };
+    Operands now, next;
+    read(0, now, a.z, false);
 #pragma unroll
     for (int k = 0; k < H; ++k) {
       f2 e[2][2];
-      advance(k, e, h4);
-      if (a.z) read_out(k, h4);
+      read(k + 1, next, a.z, false);
+      advance(now, e, h4);
+      if (a.z) read_out(k, now, h4);
+      now = next;
     }
+    float before[8];                    // dB, dC of the token behind, summed a token later
 #pragma unroll
     for (int half = 1; half >= 0; --half) {
       f2 e[H][2][2], h[H][2][2];
@@ -825,20 +850,21 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
         for (int z = 0; z < 2; ++z)
 #pragma unroll
           for (int i = 0; i < 2; ++i) h[k][z][i] = k ? h[k - 1][z][i] : half ? h4[z][i] : h0[z][i];
-        advance(half * H + k, e[k], h[k]);
-        if (half && a.z) read_out(half * H + k, h[k]);
+        if (k + 1 < H) read(half * H + k + 1, next, half && a.z, false);
+        else read(half * H + k, next, true, true);
+        advance(now, e[k], h[k]);
+        if (half && a.z) read_out(half * H + k, now, h[k]);
+        now = next;
       }
 #pragma unroll
       for (int j = H - 1; j >= 0; --j) {
         const int k = half * H + j;
-        read_again();
-        const float4 du = sm.du[k * (CB / 2) + pair];
-        const float2 g = *reinterpret_cast<const float2*>(&sm.g[k * CB + 2 * pair]);
-        const float4 B4 = *reinterpret_cast<const float4*>(&sm.B[k * SP + sl * 4]);
-        const float4 C4 = *reinterpret_cast<const float4*>(&sm.C[k * SP + sl * 4]);
-        const f2 B2[2] = {pack2(B4.x, B4.y), pack2(B4.z, B4.w)}, C2[2] = {pack2(C4.x, C4.y), pack2(C4.z, C4.w)};
-        const f2 d2[2] = {both(du.x), both(du.y)}, x2[2] = {both(du.z), both(du.w)};
-        const f2 g2[2] = {both(g.x), both(g.y)};
+        if (j > 0) read(k - 1, next, true, true);
+        else if (half) read(0, next, false, false);
+        const f2 B2[2] = {pack2(now.B.x, now.B.y), pack2(now.B.z, now.B.w)};
+        const f2 C2[2] = {pack2(now.C.x, now.C.y), pack2(now.C.z, now.C.w)};
+        const f2 d2[2] = {both(now.du.x), both(now.du.y)}, x2[2] = {both(now.du.z), both(now.du.w)};
+        const f2 g2[2] = {both(now.g.x), both(now.g.y)};
         f2 sp[2], sx[2], sb[2], sc2[2];
 #pragma unroll
         for (int z = 0; z < 2; ++z)
@@ -853,6 +879,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
             sb[i] = z ? fma2(dh, x2[z], sb[i]) : mul2(dh, x2[z]);
             sc2[i] = z ? fma2(g2[z], h[j][z][i], sc2[i]) : mul2(g2[z], h[j][z][i]);
           }
+        if (k + 1 < K) sum_channels(k + 1, before);
         // over the states: left to the per-channel pass below
         float4 px;
         float lo, hi;
@@ -865,23 +892,14 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
         unpack2(sx[1], lo, hi);
         px.w = lo + hi;
         sm.px[k * kThreads + lane_sum] = px;
-        // over the warp's channels: lane cl gets the sums from index cl * 8 / CL on
-        float v[8];                     // dB, dC of the lane's 4 states
-        unpack2(sb[0], v[0], v[1]);
-        unpack2(sb[1], v[2], v[3]);
-        unpack2(sc2[0], v[4], v[5]);
-        unpack2(sc2[1], v[6], v[7]);
-        butterfly<CL, 0, 8>(v, lane);
-        constexpr int SHARE = CL > 8 ? CL / 8 : 1, OV = CL > 8 ? 1 : 8 / CL;
-        if (cl % SHARE == 0) {
-#pragma unroll
-          for (int q = 0; q < OV; ++q) {
-            const int id = cl / SHARE * OV + q;
-            sm.w[warp][k][(id / 4) * SP + sl * 4 + id % 4] = v[q];
-          }
-        }
+        unpack2(sb[0], before[0], before[1]);
+        unpack2(sb[1], before[2], before[3]);
+        unpack2(sc2[0], before[4], before[5]);
+        unpack2(sc2[1], before[6], before[7]);
+        now = next;
       }
     }
+    sum_channels(0, before);
     __syncthreads();
     // per (token, channel)
     if (on) {
