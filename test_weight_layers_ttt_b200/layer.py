@@ -264,9 +264,12 @@ def _on_device(fn):
     current stream when none is given."""
     @functools.wraps(fn)
     def call(*args, **kw):
-        device = next((t.device for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
-        if device is None or device.type != "cuda":
+        first = args[0] if args else None
+        if not isinstance(first, torch.Tensor):
+            first = next((t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
+        if first is None or not first.is_cuda:
             return fn(*args, **kw)
+        device = first.device
         index = device.index
         if kw.get("stream") is None:
             kw["stream"] = torch._C._cuda_getCurrentRawStream(index)
@@ -339,6 +342,13 @@ def _scratch(ws, nbytes, device):
     return ws
 
 
+def _new(t):
+    """A dense tensor like ``t``, or None."""
+    if t is None:
+        return None
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _first(t, name, dims):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -373,8 +383,9 @@ def short_conv_fwd(x, w, *, bias=None, act="silu", state=None, lens=None, return
     B, N, D = x.shape
     shape = (B, desc.width - 1, D)
     if out is None:
-        out = torch.empty((B, N, D), dtype=x.dtype, device=device)
-    _dense(out, "out", (B, N, D), x.dtype, device)
+        out = _new(x)
+    else:
+        _dense(out, "out", (B, N, D), x.dtype, device)
     if state_out is None and return_state:
         state_out = torch.empty(shape, dtype=x.dtype, device=device)
     _dense(state_out, "state_out", shape, x.dtype, device)
@@ -389,8 +400,9 @@ def short_conv_step(x, w, state, *, bias=None, act="silu", out=None, stream=None
     device = _first(x, "x", 2)
     desc = _conv_desc(x, w, bias, act, state, None, (x.shape[0],))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
-    _dense(out, "out", x.shape, x.dtype, device)
+        out = _new(x)
+    else:
+        _dense(out, "out", x.shape, x.dtype, device)
     abi.ttt_short_conv_step(desc, x, w, bias, state, out, stream=stream)
     return out
 
@@ -406,10 +418,7 @@ def short_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lens=None, ds
     B, N, D = x.shape
     _dense(dy, "dy", (B, N, D), x.dtype, device)
     _dense(dstate, "dstate", (B, desc.width - 1, D), x.dtype, device)
-    dx = torch.empty((B, N, D), dtype=x.dtype, device=device)
-    dw = torch.empty_like(w)
-    dbias = None if bias is None else torch.empty_like(bias)
-    dstate_in = None if state is None else torch.empty_like(state)
+    dx, dw, dbias, dstate_in = _new(x), _new(w), _new(bias), _new(state)
     ws = _scratch(ws, abi.ttt_short_conv_bwd_workspace_bytes(desc), device)
     abi.ttt_short_conv_bwd(desc, x, w, bias, state, lens, dy, dstate, dx, dw, dbias, dstate_in,
                            ws, stream=stream)
@@ -471,9 +480,8 @@ def head_norm_rope_bwd(q, k, v, dq, dk, dv, *, wq=None, wk=None, norm="l2", eps=
             raise ValueError(f"{name} must be given exactly when its tensor is")
         if g is not None:
             _dense(g, name, (B, t.shape[2], N, h), some.dtype, device)
-    out = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
-           for t in (q, k, v)]
-    dwq, dwk = (None if w is None else torch.empty_like(w) for w in (wq, wk))
+    out = [_new(t) for t in (q, k, v)]
+    dwq, dwk = _new(wq), _new(wk)
     sums = wq is not None or wk is not None
     ws = _scratch(ws, abi.ttt_head_norm_rope_bwd_workspace_bytes(desc) if sums else 0, device)
     abi.ttt_head_norm_rope_bwd(desc, q, k, wq, wk, inv_freq, positions, dq, dk, dv, *out, dwq,
@@ -515,8 +523,9 @@ def selective_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softpl
     desc = _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, lens, tuple(u.shape[:2]))
     shape = (desc.B, desc.D, desc.S)
     if out is None:
-        out = torch.empty(u.shape, dtype=u.dtype, device=device)
-    _dense(out, "out", u.shape, u.dtype, device)
+        out = _new(u)
+    else:
+        _dense(out, "out", u.shape, u.dtype, device)
     if state_out is None and return_state:
         state_out = torch.empty(shape, dtype=torch.float32, device=device)
     _dense(state_out, "state_out", shape, torch.float32, device)
@@ -534,8 +543,9 @@ def selective_scan_step(u, dt, A, Bm, Cm, state, *, D=None, z=None, dt_bias=None
     device = _first(u, "u", 2)
     desc = _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, None, (u.shape[0],))
     if out is None:
-        out = torch.empty(u.shape, dtype=u.dtype, device=device)
-    _dense(out, "out", u.shape, u.dtype, device)
+        out = _new(u)
+    else:
+        _dense(out, "out", u.shape, u.dtype, device)
     abi.ttt_selective_scan_step(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, out,
                                 stream=stream)
     return out
@@ -552,11 +562,8 @@ def selective_scan_bwd(u, dt, A, Bm, Cm, dy, *, D=None, z=None, dt_bias=None, so
     _dense(dy, "dy", u.shape, u.dtype, device)
     _dense(dstate, "dstate", (desc.B, desc.D, desc.S), torch.float32, device)
 
-    def new(t):
-        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=device)
-
-    du, ddt, dA, dB, dC = new(u), new(dt), new(A), new(Bm), new(Cm)
-    dD, dz, dbias, dstate_in = new(D), new(z), new(dt_bias), new(state)
+    du, ddt, dA, dB, dC = _new(u), _new(dt), _new(A), _new(Bm), _new(Cm)
+    dD, dz, dbias, dstate_in = _new(D), _new(z), _new(dt_bias), _new(state)
     ws = _scratch(ws, abi.ttt_selective_scan_workspace_bytes(desc, 1), device)
     abi.ttt_selective_scan_bwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, dy, dstate,
                                du, ddt, dA, dB, dC, dD, dz, dbias, dstate_in, ws,
