@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanArgs a, int b
   using L = FwdTile<SL>;
   constexpr int TT = L::TT, CB = L::CB, SP = L::SP, EPT = L::EPT, M = L::M;
   constexpr bool AHEAD = L::BCN <= 2;   // B and C of the next tile are loaded a tile ahead
+  constexpr int UN = 4;                 // tokens in one basic block (2: 456 us, 8: 467 us, 4: 447 us
+                                        // at 8 x 2048 tokens of 4096 channels)
   __shared__ __align__(16) float2 sDU[TT * CB];            // delta; delta u
   __shared__ __align__(16) float sY[OUT ? SL * TT * CB : 4];   // each state group's sum of C h
   __shared__ __align__(16) float sB[TT * SP], sC[OUT ? TT * SP : 4];
@@ -289,9 +291,10 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanArgs a, int b
     fetch(t + TT);   // nothing behind te; unconditional, for a branch would wait for its loads
 
 #pragma unroll 1
-    for (int k0 = 0; k0 < TT; k0 += 4) {
+    for (int k0 = 0; k0 < TT; k0 += UN) {
+      float sum[UN];   // stored behind the last read: a store would hold back the reads after it
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < UN; ++j) {
         const int k = k0 + j;
         const float2 du = sDU[k * CB + cw];
         const f2 d2 = pack2(du.x, du.x), x2 = pack2(du.y, du.y);
@@ -306,8 +309,12 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanArgs a, int b
         if (OUT) {
           float lo, hi;
           unpack2(y, lo, hi);
-          sY[(k * kFwdWarps + threadIdx.x / 32) * 32 + lane] = lo + hi;
+          sum[j] = lo + hi;
         }
+      }
+      if (OUT) {
+#pragma unroll
+        for (int j = 0; j < UN; ++j) sY[((k0 + j) * kFwdWarps + threadIdx.x / 32) * 32 + lane] = sum[j];
       }
     }
     __syncthreads();
@@ -408,58 +415,79 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs a, int SP) {
 }
 
 // ---------------------------------------------------------------- one token
-// SL lanes per channel, 4 states each; the state is read and written once (HBM bound for many
-// sequences, one launch's latency for few).
-template <typename T, int SL, bool VEC>
+// SL lanes per channel, 4 states each, for NB sequences: the state is read and written once (HBM
+// bound for many sequences, one launch's latency for few). With NB > 1 a lane has that many
+// state loads in flight and reads A once for them. VEC: whole aligned runs of four states
+// everywhere. grid (channels, B / NB).
+template <typename T, int SL, bool VEC, int NB>
 __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
-  const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) / SL;
-  const int sl = threadIdx.x % SL;
-  const bool on = i < (long long)a.B * a.D;
-  const int b = on ? (int)(i / a.D) : 0, d = on ? (int)(i % a.D) : 0;
-  const int g = d / (a.D / a.G), s0 = sl * 4;
-  const float u = to_f32(static_cast<const T*>(a.u)[b * a.u_row + d]);
-  float delta = to_f32(static_cast<const T*>(a.dt)[b * a.dt_row + d]) + (a.dt_bias ? a.dt_bias[d] : 0.0f);
-  if (a.softplus) delta = softplus(delta);
-  const T* Bm = static_cast<const T*>(a.Bm) + b * a.b_row + (long long)g * a.S;
-  const T* Cm = static_cast<const T*>(a.Cm) + b * a.c_row + (long long)g * a.S;
+  const int i = blockIdx.x * (kThreads / SL) + threadIdx.x / SL, b0 = blockIdx.y * NB;
+  const int s0 = threadIdx.x % SL * 4;
+  const bool on = i < a.D;
+  const int d = on ? i : a.D - 1, g = d / (a.D / a.G);
   const float* A = a.A + (long long)d * a.S;
-  float* st = a.state_out + ((long long)b * a.D + d) * a.S;
-  float y = 0.0f, h[4];
-  if (VEC) {
-    if (s0 < a.S) {
-      float A4[4], b4[4], c4[4];
-      load_vec<float, 4>(st + s0, h);
-      load_vec<float, 4>(A + s0, A4);
+  float h[NB][4] = {}, A4[4] = {}, B4[NB][4] = {}, C4[NB][4] = {}, u[NB], z[NB], delta[NB];
+  const auto state = [&](int j) { return a.state_out + ((long long)(b0 + j) * a.D + d) * a.S + s0; };
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        b4[k] = to_f32(Bm[s0 + k]);
-        c4[k] = to_f32(Cm[s0 + k]);
+  for (int j = 0; j < NB; ++j) {
+    const int b = min(b0 + j, a.B - 1);
+    const T* Bm = static_cast<const T*>(a.Bm) + b * a.b_row + (long long)g * a.S + s0;
+    const T* Cm = static_cast<const T*>(a.Cm) + b * a.c_row + (long long)g * a.S + s0;
+    const bool live = b0 + j < a.B;
+    if constexpr (VEC) {
+      if (s0 < a.S && live) load_vec<float, 4>(state(j), h[j]);
+      if (s0 < a.S) {
+        load_input<T, 4>(Bm, B4[j]);
+        load_input<T, 4>(Cm, C4[j]);
       }
+    } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        h[k] = fmaf(ex2(delta * (A4[k] * kLog2e)), h[k], delta * u * b4[k]);
-        y = fmaf(h[k], c4[k], y);
-      }
-      if (on) store_vec<float, 4>(st + s0, h);
+      for (int k = 0; k < 4; ++k)
+        if (s0 + k < a.S) {
+          if (live) h[j][k] = state(j)[k];
+          B4[j][k] = to_f32(Bm[k]);
+          C4[j][k] = to_f32(Cm[k]);
+        }
     }
+    u[j] = to_f32(static_cast<const T*>(a.u)[b * a.u_row + d]);
+    z[j] = a.z ? to_f32(static_cast<const T*>(a.z)[b * a.z_row + d]) : 0.0f;
+    delta[j] = to_f32(static_cast<const T*>(a.dt)[b * a.dt_row + d]);
+  }
+  const float bias = a.dt_bias ? a.dt_bias[d] : 0.0f, skip = a.Dskip ? a.Dskip[d] : 0.0f;
+  if constexpr (VEC) {
+    if (s0 < a.S) load_input<float, 4>(A + s0, A4);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (s0 + k < a.S) {
-        h[k] = fmaf(ex2(delta * (A[s0 + k] * kLog2e)), st[s0 + k], delta * u * to_f32(Bm[s0 + k]));
-        y = fmaf(h[k], to_f32(Cm[s0 + k]), y);
-        if (on) st[s0 + k] = h[k];
-      }
+      if (s0 + k < a.S) A4[k] = A[s0 + k];
   }
 #pragma unroll
-  for (int m = SL / 2; m > 0; m /= 2) y += __shfl_xor_sync(0xffffffffu, y, m);
-  if (on && sl == 0) {
-    if (a.Dskip) y = fmaf(a.Dskip[d], u, y);
-    if (a.z) {
-      const float z = to_f32(static_cast<const T*>(a.z)[b * a.z_row + d]);
-      y *= z * fast_sigmoid(z);
+  for (int j = 0; j < NB; ++j) {
+    delta[j] += bias;
+    if (a.softplus) delta[j] = softplus(delta[j]);
+    float y = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      h[j][k] = fmaf(ex2(fmaf(delta[j], A4[k] * kLog2e, kExpBias)), h[j][k], delta[j] * u[j] * B4[j][k]);
+      y = fmaf(h[j][k], C4[j][k], y);
     }
-    static_cast<T*>(a.y)[(long long)b * a.D + d] = from_f32<T>(y);
+    const bool live = on && b0 + j < a.B;
+    if (live) {
+      if constexpr (VEC) {
+        if (s0 < a.S) store_vec<float, 4>(state(j), h[j]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (s0 + k < a.S) state(j)[k] = h[j][k];
+      }
+    }
+#pragma unroll
+    for (int m = SL / 2; m > 0; m /= 2) y += __shfl_xor_sync(0xffffffffu, y, m);
+    if (live && s0 == 0) {
+      y = fmaf(skip, u[j], y);
+      if (a.z) y *= z[j] * fast_sigmoid(z[j]);
+      static_cast<T*>(a.y)[(long long)(b0 + j) * a.D + d] = from_f32<T>(y);
+    }
   }
 }
 
@@ -1138,15 +1166,22 @@ cudaError_t launch(int dt, const ScanArgs& a, cudaStream_t s) {
   return dt == DT_BF16 ? launch_state<bf16, K>(a, s) : launch_state<float, K>(a, s);
 }
 
+template <typename T, int SL, bool VEC>
+cudaError_t launch_step_vec(const ScanArgs& a, cudaStream_t s) {
+  // Four sequences a lane once that still gives every SM 1024 threads.
+  const unsigned blocks = (a.D + kThreads / SL - 1) / (kThreads / SL);
+  if ((long long)blocks * (a.B / 4) >= 148 * 8)
+    scan_step_kernel<T, SL, VEC, 4><<<dim3(blocks, (a.B + 3) / 4), kThreads, 0, s>>>(a);
+  else
+    scan_step_kernel<T, SL, VEC, 1><<<dim3(blocks, a.B), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, int SL>
 cudaError_t launch_step(const ScanArgs& a, cudaStream_t s) {
-  const long long threads = (long long)a.B * a.D * SL;
-  const unsigned grid = (unsigned)((threads + kThreads - 1) / kThreads);
-  const bool vec = a.S % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state_out) |
-                                    reinterpret_cast<uintptr_t>(a.A)) % 16 == 0;
-  if (vec) scan_step_kernel<T, SL, true><<<grid, kThreads, 0, s>>>(a);
-  else scan_step_kernel<T, SL, false><<<grid, kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const bool vec = fits_four(a, a.Bm, a.b_row, sizeof(T)) && fits_four(a, a.Cm, a.c_row, sizeof(T)) &&
+                   (reinterpret_cast<uintptr_t>(a.state_out) | reinterpret_cast<uintptr_t>(a.A)) % 16 == 0;
+  return vec ? launch_step_vec<T, SL, true>(a, s) : launch_step_vec<T, SL, false>(a, s);
 }
 
 template <typename T>

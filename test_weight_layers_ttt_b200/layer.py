@@ -312,19 +312,19 @@ def _rows(t, name, lead, width, dtype, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.is_contiguous():
         return 0
-    n = 1
-    strides = t.stride()
-    for size, st in zip(reversed(width), reversed(strides[len(lead):])):
-        if size > 1 and st != n:
+    n, strides, outer = 1, t.stride(), len(lead)
+    for i in range(len(strides) - 1, outer - 1, -1):
+        size = width[i - outer]
+        if size > 1 and strides[i] != n:
             raise ValueError(f"{name}: the elements of a token must be contiguous")
         n *= size
     row = tokens = None      # the innermost of the leading sizes above 1 sets the stride
-    for size, st in zip(reversed(lead), reversed(strides[:len(lead)])):
-        if size <= 1:
+    for i in range(outer - 1, -1, -1):
+        if lead[i] <= 1:
             continue
         if row is None:
-            row, tokens = st, size
-        elif st != row * tokens:
+            row, tokens = strides[i], lead[i]
+        elif strides[i] != row * tokens:
             raise ValueError(f"{name}: all tokens must be one stride apart")
     if row is None:
         return 0
@@ -387,8 +387,9 @@ def short_conv_fwd(x, w, *, bias=None, act="silu", state=None, lens=None, return
     else:
         _dense(out, "out", (B, N, D), x.dtype, device)
     if state_out is None and return_state:
-        state_out = torch.empty(shape, dtype=x.dtype, device=device)
-    _dense(state_out, "state_out", shape, x.dtype, device)
+        state_out = x.new_empty(shape)
+    else:
+        _dense(state_out, "state_out", shape, x.dtype, device)
     abi.ttt_short_conv_fwd(desc, x, w, bias, state, lens, out, state_out, stream=stream)
     return out, state_out
 
@@ -459,9 +460,7 @@ def head_norm_rope_fwd(q, k, v=None, *, wq=None, wk=None, norm="l2", eps=1e-6, i
     int32, or pos0 + t), and v laid out. Returns (q, k, v)."""
     desc, some = _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs)
     B, N, _, h = some.shape
-    out = [None if t is None else
-           torch.empty((B, t.shape[2], N, h), dtype=t.dtype, device=some.device)
-           for t in (q, k, v)]
+    out = [None if t is None else t.new_empty((B, t.shape[2], N, h)) for t in (q, k, v)]
     abi.ttt_head_norm_rope_fwd(desc, q, k, v, wq, wk, inv_freq, positions, *out, stream=stream)
     return tuple(out)
 
@@ -527,8 +526,9 @@ def selective_scan_fwd(u, dt, A, Bm, Cm, *, D=None, z=None, dt_bias=None, softpl
     else:
         _dense(out, "out", u.shape, u.dtype, device)
     if state_out is None and return_state:
-        state_out = torch.empty(shape, dtype=torch.float32, device=device)
-    _dense(state_out, "state_out", shape, torch.float32, device)
+        state_out = A.new_empty(shape)
+    else:
+        _dense(state_out, "state_out", shape, torch.float32, device)
     ws = _scratch(ws, abi.ttt_selective_scan_workspace_bytes(desc, 0), device)
     abi.ttt_selective_scan_fwd(desc, u, dt, A, Bm, Cm, D, z, dt_bias, state, lens, out,
                                state_out, ws, stream=stream)
