@@ -737,13 +737,20 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
   }
   const int lane_sum = sum_slot<CL>(warp, sl, cl);
 
-  const T* const src[4] = {static_cast<const T*>(a.u) + sc, static_cast<const T*>(a.dt) + sc,
-                           static_cast<const T*>(a.z) + sc, static_cast<const T*>(a.dy) + sc};
+  const int last = te > t0 ? (te - 1 - t0) / K * K + t0 : t0 - K;   // first token of the last 8
+  // the next 8 tokens' rows, walked backwards
+  const T* src[4];
+  long long stride[4] = {a.u_row, a.dt_row, a.z_row, a.D};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const void* p = i == 0 ? a.u : i == 1 ? a.dt : i == 2 ? a.z : a.dy;
+    src[i] = static_cast<const T*>(p) + (seq + last + row) * stride[i] + sc;
+    stride[i] *= K;
+  }
   Raw<T, EPT, false> regs[VEC ? 1 : 4];
   // the operands of the 8 tokens from t on (none in front of t0 or behind te) into buffer `buf`
   const auto fetch = [&](int t, int buf) {
     const int k = t + row, ok = t >= t0 && k < te ? valid : 0;
-    const long long at[4] = {(seq + k) * a.u_row, (seq + k) * a.dt_row, (seq + k) * a.z_row, (seq + k) * a.D};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (i == 2 && !a.z) continue;
@@ -751,10 +758,11 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
         constexpr int BYTES = EPT * sizeof(T) > 16 ? 16 : EPT * (int)sizeof(T);
 #pragma unroll
         for (int q = 0; q < EPT * (int)sizeof(T) / BYTES; ++q)
-          copy_async<BYTES>(&sm.raw[buf][i][slot + q * BYTES / sizeof(T)], src[i] + at[i] + q * BYTES / sizeof(T), ok > 0);
+          copy_async<BYTES>(&sm.raw[buf][i][slot + q * BYTES / sizeof(T)], src[i] + q * BYTES / sizeof(T), ok > 0);
       } else {
-        regs[i].load(src[i] + at[i], ok);
+        regs[i].load(src[i], ok);
       }
+      src[i] -= stride[i];
     }
     const long long mark = ((long long)b * subs + t / K) * a.D + r.c0;
     const bool in = t >= t0 && t < te;
@@ -782,7 +790,6 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
       }
     }
   };
-  const int last = te > t0 ? (te - 1 - t0) / K * K + t0 : t0 - K;   // first token of the last 8
   int buf = 0;
   if (last >= t0) fetch(last, 0);
   for (int t = last; t >= t0; t -= K, buf ^= 1) {
@@ -967,59 +974,82 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
     if (on) {
       float u[EPT], raw[EPT], dy[EPT], z[EPT], p[EPT], x[EPT], y[EPT], delta[EPT];
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) p[i] = x[i] = y[i] = 0.0f;
-#pragma unroll
       for (int i = 0; i < EPT; i += 2) {
         const int ch = col + i;
+        f2 p2 = 0, x2 = 0, y2 = 0;
 #pragma unroll
         for (int q = 0; q < SL; ++q) {
           const int at = row * kThreads + sum_slot<CL>(ch / L::WC, q, ch % L::WC / 2);
           const float4 v = sm.px[at];
-          const float2 w = a.z ? sm.y[at] : make_float2(0.0f, 0.0f);
-          if constexpr (EPT == 1) {
-            p[0] += ch % 2 ? v.y : v.x;
-            x[0] += ch % 2 ? v.w : v.z;
-            y[0] += ch % 2 ? w.y : w.x;
-          } else {
-            p[i] += v.x;
-            p[i + 1] += v.y;
-            x[i] += v.z;
-            x[i + 1] += v.w;
-            y[i] += w.x;
-            y[i + 1] += w.y;
-          }
+          p2 = add2(p2, pack2(v.x, v.y));
+          x2 = add2(x2, pack2(v.z, v.w));
+          if (a.z) y2 = add2(y2, *reinterpret_cast<const f2*>(&sm.y[at]));
         }
         const float4 du = sm.du[(slot + i) / 2];
+        float lo[4], hi[4] = {0.0f, 0.0f, 0.0f, du.y};
+        unpack2(p2, lo[0], hi[0]);
+        unpack2(x2, lo[1], hi[1]);
+        unpack2(y2, lo[2], hi[2]);
+        lo[3] = du.x;
         if constexpr (EPT == 1) {
-          delta[0] = ch % 2 ? du.y : du.x;
+          p[0] = ch % 2 ? hi[0] : lo[0];
+          x[0] = ch % 2 ? hi[1] : lo[1];
+          y[0] = ch % 2 ? hi[2] : lo[2];
+          delta[0] = ch % 2 ? hi[3] : lo[3];
         } else {
-          delta[i] = du.x;
-          delta[i + 1] = du.y;
+          p[i] = lo[0];
+          p[i + 1] = hi[0];
+          x[i] = lo[1];
+          x[i + 1] = hi[1];
+          y[i] = lo[2];
+          y[i + 1] = hi[2];
+          delta[i] = lo[3];
+          delta[i + 1] = hi[3];
         }
       }
-      float g[EPT], skip[EPT], bias[EPT], acc[2][EPT];
+      float g[EPT], skip[EPT], bias[EPT], acc[2][EPT], o1[EPT], o2[EPT], o3[EPT];
       load_vec<T, EPT>(&sm.raw[buf][0][slot], u);
       load_vec<T, EPT>(&sm.raw[buf][1][slot], raw);
-      load_vec<T, EPT>(&sm.raw[buf][3][slot], dy);
-      if (a.z) load_vec<T, EPT>(&sm.raw[buf][2][slot], z);
       load_vec<float, EPT>(&sm.g[slot], g);
       load_vec<float, EPT>(&sm.bias[col], bias);
       load_vec<float, EPT>(&sm.skip[col], skip);
       load_vec<float, EPT>(&sm.acc[0][slot], acc[0]);
       load_vec<float, EPT>(&sm.acc[1][slot], acc[1]);
+      mul_v<EPT>(o1, delta, x);
+      fma_v<EPT>(o1, skip, g, o1);               // du
+      mul_v<EPT>(o2, p, kLn2);
+      fma_v<EPT>(o2, u, x, o2);                  // the gradient of delta
+      if (a.softplus) {
+        float sg[EPT];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) sg[i] = fast_sigmoid(raw[i] + bias[i]);
+        mul_v<EPT>(o2, o2, sg);
+      }
+      fma_v<EPT>(acc[0], g, u, acc[0]);
+      fma_v<EPT>(acc[1], o2, 1.0f, acc[1]);
       Raw<T, EPT, VEC> odu, odt, odz;
 #pragma unroll
       for (int i = 0; i < EPT; ++i) {
-        odu.set(i, fmaf(skip[i], g[i], delta[i] * x[i]));
-        float dd = fmaf(u[i], x[i], p[i] * kLn2);
-        if (a.softplus) dd *= fast_sigmoid(raw[i] + bias[i]);
-        odt.set(i, dd);
-        acc[0][i] = fmaf(g[i], u[i], acc[0][i]);
-        acc[1][i] += dd;
-        if (a.z) {
-          const float sg = fast_sigmoid(z[i]);
-          odz.set(i, dy[i] * fmaf(skip[i], u[i], y[i]) * sg * fmaf(z[i], 1.0f - sg, 1.0f));
+        odu.set(i, o1[i]);
+        odt.set(i, o2[i]);
+      }
+      if (a.z) {                                 // dz = dy y silu'(z), silu' = s (1 + z (1 - s))
+        load_vec<T, EPT>(&sm.raw[buf][3][slot], dy);
+        load_vec<T, EPT>(&sm.raw[buf][2][slot], z);
+        float sg[EPT], ns[EPT], one[EPT];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+          sg[i] = fast_sigmoid(z[i]);
+          ns[i] = 1.0f - sg[i];
+          one[i] = 1.0f;
         }
+        fma_v<EPT>(y, skip, u, y);
+        fma_v<EPT>(o3, z, ns, one);
+        mul_v<EPT>(o3, o3, sg);
+        mul_v<EPT>(y, y, dy);
+        mul_v<EPT>(o3, o3, y);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) odz.set(i, o3[i]);
       }
       store_vec<float, EPT>(&sm.acc[0][slot], acc[0]);
       store_vec<float, EPT>(&sm.acc[1][slot], acc[1]);
