@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
       if (in.kind < 3) in.next(a, first, step, minor_step, BWD ? major_step : 0, source);
     };
     fetch();
-    float cs[E][V], sn[E][V], wa[E][V], wb[E][V];
+    float cs[E][V], sn[E][V], ns[E][V], wa[E][V], wb[E][V];   // cos, sin, -sin, weights
     const double pos = !live ? 0.0 : a.positions ? (double)a.positions[m] : (double)(a.pos0 + t);
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -201,8 +201,10 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
           turn -= rint(turn);
           sincospif((float)(2.0 * turn), &sn[e][q], &cs[e][q]);
         }
+        ns[e][q] = -sn[e][q];
       }
     int kind = -1;
+    bool scaled = false;
     while (out.kind < 3) {
       float xa[R][E][V], xb[R][E][V], ga[R][E][V], gb[R][E][V];
 #pragma unroll
@@ -232,6 +234,7 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
       if (out.kind != kind) {           // the first rows of q or k
         kind = out.kind;
         const float* w = a.w[kind];
+        scaled = w != nullptr;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
 #pragma unroll
@@ -243,32 +246,32 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
       }
 #pragma unroll
       for (int z = 0; z < R; ++z) {
-        float r = 1.0f, back = 0.0f, ss[V] = {}, dot[V] = {};
+        float r = 1.0f, back = 0.0f, ss[V] = {}, dot[V] = {}, gwa[E][V], gwb[E][V];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
           fma_v<V>(ss, xa[z][e], xa[z][e], ss);
           fma_v<V>(ss, xb[z][e], xb[z][e], ss);
-          if (BWD) {   // the rotation's transpose
-            float u[V], v[V], ns[V];
-#pragma unroll
-            for (int q = 0; q < V; ++q) ns[q] = -sn[e][q];
-            mul_v<V>(u, ga[z][e], ns);
+          if (BWD) {   // the rotation's transpose, then the weights
+            float u[V], v[V];
+            mul_v<V>(u, ga[z][e], ns[e]);
             mul_v<V>(v, gb[z][e], sn[e]);
             fma_v<V>(ga[z][e], ga[z][e], cs[e], v);
             fma_v<V>(gb[z][e], gb[z][e], cs[e], u);
-            mul_v<V>(u, ga[z][e], wa[e]);
-            mul_v<V>(v, gb[z][e], wb[e]);
-            fma_v<V>(dot, u, xa[z][e], dot);
-            fma_v<V>(dot, v, xb[z][e], dot);
+#pragma unroll
+            for (int q = 0; q < V; ++q) {
+              gwa[e][q] = ga[z][e][q];
+              gwb[e][q] = gb[z][e][q];
+            }
+            if (scaled) {
+              mul_v<V>(gwa[e], ga[z][e], wa[e]);
+              mul_v<V>(gwb[e], gb[z][e], wb[e]);
+            }
+            fma_v<V>(dot, gwa[e], xa[z][e], dot);
+            fma_v<V>(dot, gwb[e], xb[z][e], dot);
           }
         }
         if (a.norm != TTT_NORM_NONE) {
-          float s = 0.0f, d = 0.0f;
-#pragma unroll
-          for (int q = 0; q < V; ++q) {
-            s += ss[q];
-            d += dot[q];
-          }
+          const float s = sum_v<V>(ss), d = BWD ? sum_v<V>(dot) : 0.0f;
           r = rsqrtf(fmaf(group_sum(s, lanes), inv_h, a.eps));
           if (BWD) back = -r * r * r * group_sum(d, lanes) * inv_h;
         }
@@ -276,14 +279,13 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
         for (int e = 0; e < E; ++e) {
           float oa[V], ob[V], u[V], v[V];
           if constexpr (!BWD) {
-            float ns[V];
-#pragma unroll
-            for (int q = 0; q < V; ++q) ns[q] = -sn[e][q];
             mul_v<V>(u, xa[z][e], r);
             mul_v<V>(v, xb[z][e], r);
-            mul_v<V>(u, u, wa[e]);
-            mul_v<V>(v, v, wb[e]);
-            mul_v<V>(oa, v, ns);
+            if (scaled) {
+              mul_v<V>(u, u, wa[e]);
+              mul_v<V>(v, v, wb[e]);
+            }
+            mul_v<V>(oa, v, ns[e]);
             mul_v<V>(ob, u, sn[e]);
             fma_v<V>(oa, u, cs[e], oa);
             fma_v<V>(ob, v, cs[e], ob);
@@ -291,10 +293,8 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
             // dx = r (g w) - x r^3 <g w, x> [/ h];  dw += g (x r)
             mul_v<V>(oa, xa[z][e], back);
             mul_v<V>(ob, xb[z][e], back);
-            mul_v<V>(u, ga[z][e], wa[e]);
-            mul_v<V>(v, gb[z][e], wb[e]);
-            fma_v<V>(oa, u, r, oa);
-            fma_v<V>(ob, v, r, ob);
+            fma_v<V>(oa, gwa[e], r, oa);
+            fma_v<V>(ob, gwb[e], r, ob);
             if (a.partials) {
               mul_v<V>(u, xa[z][e], r);
               mul_v<V>(v, xb[z][e], r);

@@ -69,6 +69,19 @@ __device__ __forceinline__ void fma_v(float (&o)[V], const float (&a)[V], float 
   }
 }
 
+template <int V>
+__device__ __forceinline__ float sum_v(const float (&a)[V]) {
+  if constexpr (V == 1) return a[0];
+  else if constexpr (V == 2) return a[0] + a[1];
+  else {
+    float h[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; i += 2)
+      unpack2(add2(pack2(a[i], a[i + 1]), pack2(a[V / 2 + i], a[V / 2 + i + 1])), h[i], h[i + 1]);
+    return sum_v<V / 2>(h);
+  }
+}
+
 // V consecutive elements in one access (V * sizeof(T) in {2, 4, 8, 16} bytes and aligned to
 // that).
 template <typename T, int V> struct Pack;
@@ -140,6 +153,12 @@ __device__ __forceinline__ void load_vec(const T* p, float (&f)[V]) {
   }
 }
 
+// Two values rounded to bf16 in one instruction.
+__device__ __forceinline__ unsigned bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const unsigned*>(&v);
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
   if constexpr (V * sizeof(T) > 16) {
@@ -153,9 +172,14 @@ __device__ __forceinline__ void store_vec(T* p, const float (&f)[V]) {
     store_vec<T, V / 2>(p + V / 2, hi);
     return;
   } else {
-    union { typename Pack<T, V>::U u; T t[V]; } x;
+    union { typename Pack<T, V>::U u; T t[V]; unsigned w[(V * sizeof(T) + 3) / 4]; } x;
+    if constexpr (sizeof(T) == 2 && V > 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) x.t[i] = from_f32<T>(f[i]);
+      for (int i = 0; i < V; i += 2) x.w[i / 2] = bf16_pair(f[i], f[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) x.t[i] = from_f32<T>(f[i]);
+    }
     *reinterpret_cast<typename Pack<T, V>::U*>(p) = x.u;
   }
 }

@@ -82,6 +82,7 @@ template <typename T, int N, bool VEC> struct Raw {
     T t[N];
     typename Pack<T, W>::U u[N / W];
     typename Pack<T, 1>::U e[N];
+    unsigned w[(N * sizeof(T) + 3) / 4];
   };
   __device__ __forceinline__ void load(const T* p, int valid) {
     if constexpr (VEC) {
@@ -107,6 +108,14 @@ template <typename T, int N, bool VEC> struct Raw {
   }
   __device__ __forceinline__ float get(int i) const { return to_f32(t[i]); }
   __device__ __forceinline__ void set(int i, float v) { t[i] = from_f32<T>(v); }
+  __device__ __forceinline__ void set_pair(int i, float lo, float hi) {   // i even
+    if constexpr (VEC && sizeof(T) == 2 && N > 1) {
+      w[i / 2] = bf16_pair(lo, hi);
+    } else {
+      t[i] = from_f32<T>(lo);
+      if constexpr (N > 1) t[i + 1] = from_f32<T>(hi);
+    }
+  }
 };
 
 // A block's channels: block cb of group g covers c0 .. c1 - 1.
@@ -334,8 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanArgs a, int b
         }
         float y0, y1;
         unpack2(y, y0, y1);
-        out.set(i, y0);
-        out.set(i + 1, y1);
+        out.set_pair(i, y0, y1);
       }
       out.store(py, valid);
     }
@@ -1029,9 +1037,9 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
       fma_v<EPT>(acc[1], o2, 1.0f, acc[1]);
       Raw<T, EPT, VEC> odu, odt, odz;
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        odu.set(i, o1[i]);
-        odt.set(i, o2[i]);
+      for (int i = 0; i < EPT; i += 2) {
+        odu.set_pair(i, o1[i], o1[EPT > 1 ? i + 1 : i]);
+        odt.set_pair(i, o2[i], o2[EPT > 1 ? i + 1 : i]);
       }
       if (a.z) {                                 // dz = dy y silu'(z), silu' = s (1 + z (1 - s))
         load_vec<T, EPT>(&sm.raw[buf][3][slot], dy);
@@ -1049,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
         mul_v<EPT>(y, y, dy);
         mul_v<EPT>(o3, o3, y);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) odz.set(i, o3[i]);
+        for (int i = 0; i < EPT; i += 2) odz.set_pair(i, o3[i], o3[EPT > 1 ? i + 1 : i]);
       }
       store_vec<float, EPT>(&sm.acc[0][slot], acc[0]);
       store_vec<float, EPT>(&sm.acc[1][slot], acc[1]);
