@@ -260,23 +260,29 @@ PAIRS = {"halves": abi.TTT_PAIRS_HALVES, "interleaved": abi.TTT_PAIRS_INTERLEAVE
 
 
 def _on_device(fn):
-    """Runs ``fn`` with the device of its first tensor as the current one, and on that device's
-    current stream when none is given."""
+    """Runs ``fn`` with the device of its first tensor as the current one, on that device's
+    current stream, or on ``stream`` with what the call allocates belonging to it (memory of
+    another stream could be handed out again while the kernels still run)."""
     @functools.wraps(fn)
-    def call(*args, **kw):
+    def call(*args, stream=None, **kw):
         first = args[0] if args else None
         if not isinstance(first, torch.Tensor):
             first = next((t for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), None)
         if first is None or not first.is_cuda:
-            return fn(*args, **kw)
-        device = first.device
-        index = device.index
-        if kw.get("stream") is None:
-            kw["stream"] = torch._C._cuda_getCurrentRawStream(index)
+            return fn(*args, stream=stream, **kw)
+        index = first.device.index
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=first.device)
+            if stream.device_index != index:
+                raise ValueError(f"stream is of device {stream.device_index}, the tensors of {index}")
+            with torch.cuda.stream(stream):
+                return fn(*args, stream=stream.cuda_stream, **kw)
+        raw = torch._C._cuda_getCurrentRawStream(index)
         if index == torch._C._cuda_getDevice():
-            return fn(*args, **kw)
-        with torch.cuda.device(device):
-            return fn(*args, **kw)
+            return fn(*args, stream=raw, **kw)
+        with torch.cuda.device(index):
+            return fn(*args, stream=raw, **kw)
     return call
 
 

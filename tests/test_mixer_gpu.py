@@ -117,6 +117,18 @@ def test_short_conv_steps_equal_the_prompt(dtype, B, D, width):
     assert torch.equal(state, new)
 
 
+def test_short_conv_without_bias_and_state():
+    x, w, _, _, xg, wg, _, rng = conv_case("bf16", 2, 50, 24, 4, "silu", False, None, 0, seed=5)
+    y, none = layer.short_conv_fwd(xg, wg, return_state=False)
+    near(y, M.short_conv(x, w)[0], 48)
+    dy = rand(rng, 2, 50, 24, dtype="bf16")
+    dx, dw, db, ds = layer.short_conv_bwd(xg, wg, dev(dy, torch.bfloat16))
+    ref = M.short_conv_backward(x, w, dy)
+    near(dx, ref[0], 64)
+    near(dw, ref[1], 164)
+    assert none is None and db is None and ds is None
+
+
 # ----------------------------------------------------------------------------- heads
 HEADS = [  # dtype, B, N, (Hq, Hk, Hv), h, norm, weight, rot, pairs, far, pad
     ("bf16", 2, 37, (4, 2, 2), 128, "l2", False, 128, "halves", 0, 0),
@@ -200,6 +212,23 @@ def test_head_norm_rope_default_positions_and_zero_rows():
     pos = np.broadcast_to(np.arange(6) + 4, (2, 6))
     near(q, M.head_norm_rope(x, None, "l2", 1e-6, inv, pos), 64)
     assert k is None and v is None and host(q)[1, 1, 2].max() == 0.0
+
+
+@pytest.mark.parametrize("which", [(False, True, False), (False, False, True), (True, False, True)])
+def test_head_norm_rope_of_some_tensors(which):
+    xs, ws, xg, kw, ok, rng = heads_case("bf16", 2, 23, (3, 2, 4), 64, "rms", True, 32, "halves", 9, 0)
+    xg = [x if on else None for x, on in zip(xg, which)]
+    out = layer.head_norm_rope_fwd(*xg, **kw)
+    back = layer.head_norm_rope_bwd(*xg, *out, **kw)
+    for i, on in enumerate(which):
+        assert (out[i] is not None) == on and (back[i] is not None) == on
+        if on and i < 2:
+            near(out[i], M.head_norm_rope(xs[i], ws[i], **ok), 96)
+            dx, dw = M.head_norm_rope_backward(xs[i], host(out[i]), ws[i], **ok)
+            near(back[i], dx, 320, terms=8 * 2 * 4)      # sqrt(64) 2 |dout| |w| r, all below 2
+            near(back[3 + i], dw, 2 * 23 * 4 + 128)
+        elif on:
+            assert torch.equal(out[i], xg[i].transpose(1, 2)) and torch.equal(back[i], xg[i])
 
 
 # ----------------------------------------------------------------------------- selective scan
@@ -318,6 +347,47 @@ def test_a_split_sequence_equals_two_calls():
     near(state, hs[:, -1], scan_roundings(900, 16))
 
 
+def test_selective_scan_without_options():
+    """No skip, gate, bias or state, and delta as it is."""
+    h, g, rng = scan_case("fp32", 2, 70, 12, 16, 1, False, False, None, False, 0, seed=13)
+    for k in ("D", "dt_bias"):
+        h.pop(k), g.pop(k)
+    y, none = layer.selective_scan_fwd(**g, return_state=False)
+    near(y, M.selective_scan(**h)[0], scan_roundings(70, 16))
+    dy = rand(rng, 2, 70, 12)
+    got = layer.selective_scan_bwd(**g, dy=dev(dy))
+    ref = M.selective_scan_backward(**h, dy=dy)
+    for t, name in zip(got, ("du", "ddt", "dA", "dB", "dC")):
+        near(t, ref[name], 2 * scan_roundings(70, 16) + 140, name)
+    assert none is None and all(t is None for t in got[5:])
+
+
+@pytest.mark.parametrize("dtype,B,D,S", [("bf16", 77, 2048, 16), ("fp32", 131, 1100, 7), ("bf16", 5, 9, 64)])
+def test_selective_scan_step_of_many_sequences(dtype, B, D, S):
+    rng = np.random.default_rng(17)
+    h, g, _ = scan_case(dtype, B, 1, D, S, 1, True, True, None, True, 3, seed=17)
+    ry, hs = M.selective_scan(**h)
+    tokens = ("u", "dt", "z", "Bm", "Cm")
+    g.pop("softplus")
+    y = layer.selective_scan_step(**{k: v[:, 0] if k in tokens else v for k, v in g.items()})
+    near(y, ry[:, 0], scan_roundings(1, S))
+    near(g["state"], hs[:, -1], scan_roundings(1, S))
+
+
+@pytest.mark.parametrize("n", [1, 30, 257])
+def test_padded_sequences_equal_their_own_calls(n):
+    """A padded batch against calls of the sequences alone (which may be cut elsewhere)."""
+    h, g, rng = scan_case("fp32", 2, 300, 40, 16, 1, True, True, [n, 300], True, 0, seed=21)
+    y, st = layer.selective_scan_fwd(**g)
+    one = {k: v[:1] if k in ("state",) else v[:1, :n].contiguous() if k in ("u", "dt", "z", "Bm", "Cm") else v
+           for k, v in g.items() if k != "lens"}
+    y1, st1 = layer.selective_scan_fwd(**one)
+    top = float(y1.abs().max())
+    assert float((y[:1, :n] - y1).abs().max()) <= scan_roundings(n, 16) * U * top
+    assert float((st[:1] - st1).abs().max()) <= scan_roundings(n, 16) * U * float(st1.abs().max())
+    assert float(y[0, n:].abs().max()) == 0.0 if n < 300 else True
+
+
 # ----------------------------------------------------------------------------- how they are called
 def together(g):
     """Projection -> short convolution -> heads -> the layer's linear attention and, beside it,
@@ -401,6 +471,26 @@ def test_the_same_call_gives_the_same_bits_on_streams_and_in_graphs():
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for _, out in graphs for a, b in zip(first, out))
+
+
+def test_a_given_stream_is_used():
+    """stream= as a torch stream and as a raw handle; the results are ready when it is."""
+    g = together_inputs()
+    x, w = g["x"], g["w"][:, :96].contiguous()
+    y0, s0 = layer.short_conv_fwd(x, w)
+    u, A = x[..., :64].contiguous(), g["A"][:64].contiguous()
+    bc = x[..., 64:80].unsqueeze(2).contiguous()
+    r0 = layer.selective_scan_bwd(u, u, A, bc, bc, u)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        y1, s1 = layer.short_conv_fwd(x, w, stream=stream)
+        r1 = layer.selective_scan_bwd(u, u, A, bc, bc, u, stream=stream)
+        junk = [torch.full((1 << 20,), float("nan"), device="cuda") for _ in range(8)]   # on the other stream
+        s.synchronize()
+        assert torch.equal(y0, y1) and torch.equal(s0, s1)
+        assert all(torch.equal(a, b) for a, b in zip(r0[:5], r1[:5]))
+        del junk
 
 
 def test_debug_checks_cover_the_operators():
