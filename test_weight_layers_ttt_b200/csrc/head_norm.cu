@@ -18,10 +18,12 @@ namespace ttt {
 namespace {
 
 constexpr int kHeadThreads = 128;
-// Blocks of an SM: what the registers leave (128 a thread forward, 168 backward, where the two
-// weight gradients stay in them), which at 16 lanes a row of 256 elements keeps 16 (12) KB of
-// loads in flight per SM.
-constexpr int kFwdBlocks = 4, kBwdBlocks = 3;
+// Blocks of an SM (what the registers leave; the backward keeps two weight gradients in them)
+// and rows that each thread has on their way. Two lm-sized tensors' forward of 256 elements a
+// head: 162 us with one row ahead in registers, 145 us with 4 blocks of 4 rows, 137 us with 6 of
+// 3; backward at 128: 320 us in registers, 224 us with 3 blocks of 3, 308 us with 4 blocks (spills).
+constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
+constexpr int kFwdRows = 3, kBwdRows = 3;
 constexpr double kInvTwoPi = 0.15915494309189533576888;
 
 enum : int { PAIRS_HALVES = 0, PAIRS_INTERLEAVED = 1 };
@@ -97,10 +99,10 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// A walk over the rows of a group's token: the heads of q, then of k, then of v, in batches of R
-// rows `step` heads apart. All groups of a block walk alike (head - first is the same), whether
-// or not their token and head exist.
-template <typename T, int R>
+// A walk over the rows of a group's token: the heads of q, then of k, then of v, `step` heads
+// apart. All groups of a block walk alike (head - first is the same), whether or not their token
+// and head exist.
+template <typename T>
 struct Walk {
   int kind = 0, head = 0;
   T* p[2];          // this head's row in one or two tensors
@@ -117,24 +119,38 @@ struct Walk {
   }
   template <typename F>
   __device__ __forceinline__ void next(const HeadArgs& a, int first, int step, long long s0, long long s1, F&& start) {
-    head += R * step;
-    p[0] += R * s0;
-    p[1] += R * s1;
+    head += step;
+    p[0] += s0;
+    p[1] += s1;
     if (head - first >= a.H[kind]) enter(a, kind + 1, first, start);
   }
+};
+
+// A thread's rows on their way: `depth` of them, `items` accesses each, at most 256 bytes of
+// shared memory.
+template <typename T, int V, int E, bool BWD> struct Ring {
+  static constexpr bool on = V * sizeof(T) >= 4;
+  static constexpr int items = E * (BWD ? 4 : 2), bytes = items * V * (int)sizeof(T);
+  static constexpr int most = BWD ? kBwdRows : kFwdRows;
+  static constexpr int depth = !on ? 1 : most * bytes <= 256 ? most : 256 / bytes;
 };
 
 // A tile is 2^log_tile tokens: group g takes token g % tile and every (groups / tile)-th head of
 // it, so that a lane takes the angles of its pairs once for all heads, into registers, and
 // neighbouring groups write neighbouring rows of the head-major output. E runs of V pairs per
-// lane, `lanes` lanes per row. The next batch of rows is loaded before the current one is used,
-// and the first before the angles are taken. Dynamic shared memory in the backward with
-// weights: float[2][h].
+// lane, `lanes` lanes per row. The first rows are on their way before the angles are taken.
+// Dynamic shared memory: in the backward float[2][h], then the ring of rows.
 template <typename T, int V, int PAIRS, int E, bool BWD>
 __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks : kFwdBlocks) : 1)
     head_kernel(HeadArgs a, int log_tile, int lanes) {
-  extern __shared__ float acc[];
-  constexpr int R = BWD || E > 2 ? 1 : 2;   // rows of a batch
+  extern __shared__ __align__(16) float acc[];
+  // The rows on their way: DEPTH of them in shared memory by asynchronous copies, each thread's
+  // own, where an access has the 4 bytes that such a copy takes at least; else one in registers.
+  using L = Ring<T, V, E, BWD>;
+  constexpr bool RING = L::on;
+  constexpr int DEPTH = L::depth, ITEMS = L::items;
+  using U = typename Pack<T, V>::U;
+  U* const ring = reinterpret_cast<U*>(reinterpret_cast<char*>(acc) + (BWD ? 2 * a.h * 4 + 15 & ~15 : 0)) + threadIdx.x;
   const int M = a.B * a.N, half = a.rot / 2, npairs = (a.h + 1) / 2;
   const int lane = threadIdx.x % lanes, group = threadIdx.x / lanes;
   const int first = group >> log_tile, step = (kHeadThreads / lanes) >> log_tile;
@@ -166,27 +182,38 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
     const auto target = [&](int k, int) {
       return BWD ? static_cast<T*>(a.dx[k]) + (m * a.H[k] + first) * a.h : static_cast<T*>(a.out[k]) + major_row(k);
     };
-    Walk<const T, R> in;
-    Walk<T, R> out;
+    Walk<const T> in;
+    Walk<T> out;
     in.enter(a, 0, first, source);
     out.enter(a, 0, first, target);
-    RawPairs<T, V> rx[R][E], rg[BWD ? R : 1][E];
+    RawPairs<T, V> rx[E], rg[E];
+    int put = 0, take = 0;              // ring entries
     const auto fetch = [&]() {
-      const bool any = in.kind < 3 && live;
-      const int H = in.kind < 3 ? a.H[in.kind] : 0;
+      const bool row = in.kind < 3 && live && in.head < a.H[in.kind < 3 ? in.kind : 0];
 #pragma unroll
-      for (int z = 0; z < R; ++z) {
-        const bool row = any && in.head + z * step < H;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const bool x = row && (!BWD || in.kind < 2);
-          load_raw_pairs<T, V>(rx[z][e], in.p[0] + z * minor_step, lo[e], hi[e], x && on[e], x && on_hi[e]);
-          if (BWD) load_raw_pairs<T, V>(rg[z][e], in.p[1] + z * major_step, lo[e], hi[e], row && on[e], row && on_hi[e]);
+      for (int e = 0; e < E; ++e) {
+        const bool x = row && (!BWD || in.kind < 2);
+        if constexpr (RING) {
+          U* q = ring + (put * ITEMS + e * (BWD ? 4 : 2)) * kHeadThreads;
+          copy_async<sizeof(U)>(q, in.p[0] + lo[e], x && on[e]);
+          copy_async<sizeof(U)>(q + kHeadThreads, in.p[0] + hi[e], x && on_hi[e]);
+          if (BWD) {
+            copy_async<sizeof(U)>(q + 2 * kHeadThreads, in.p[1] + lo[e], row && on[e]);
+            copy_async<sizeof(U)>(q + 3 * kHeadThreads, in.p[1] + hi[e], row && on_hi[e]);
+          }
+        } else {
+          load_raw_pairs<T, V>(rx[e], in.p[0], lo[e], hi[e], x && on[e], x && on_hi[e]);
+          if (BWD) load_raw_pairs<T, V>(rg[e], in.p[1], lo[e], hi[e], row && on[e], row && on_hi[e]);
         }
+      }
+      if constexpr (RING) {
+        copies_commit();
+        put = put + 1 == DEPTH ? 0 : put + 1;
       }
       if (in.kind < 3) in.next(a, first, step, minor_step, BWD ? major_step : 0, source);
     };
-    fetch();
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) fetch();
     float cs[E][V], sn[E][V], ns[E][V], wa[E][V], wb[E][V];   // cos, sin, -sin, weights
     const double pos = !live ? 0.0 : a.positions ? (double)a.positions[m] : (double)(a.pos0 + t);
 #pragma unroll
@@ -206,28 +233,37 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
     int kind = -1;
     bool scaled = false;
     while (out.kind < 3) {
-      float xa[R][E][V], xb[R][E][V], ga[R][E][V], gb[R][E][V];
-#pragma unroll
-      for (int z = 0; z < R; ++z)
+      float xa[E][V], xb[E][V], ga[E][V], gb[E][V];
+      if constexpr (RING) {
+        copies_wait_but<DEPTH - 1>();
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          unpack_pairs<T, V, PAIRS>(rx[z][e], xa[z][e], xb[z][e]);
-          if (BWD) unpack_pairs<T, V, PAIRS>(rg[z][e], ga[z][e], gb[z][e]);
+          const U* q = ring + (take * ITEMS + e * (BWD ? 4 : 2)) * kHeadThreads;
+          rx[e].a = q[0];
+          rx[e].b = q[kHeadThreads];
+          if (BWD) {
+            rg[e].a = q[2 * kHeadThreads];
+            rg[e].b = q[3 * kHeadThreads];
+          }
         }
+        take = take + 1 == DEPTH ? 0 : take + 1;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        unpack_pairs<T, V, PAIRS>(rx[e], xa[e], xb[e]);
+        if (BWD) unpack_pairs<T, V, PAIRS>(rg[e], ga[e], gb[e]);
+      }
       fetch();
       const int H = a.H[out.kind];
-      const auto write = [&](int z, int e, const float (&u)[V], const float (&v)[V]) {
-        if (live && out.head + z * step < H && on[e])
-          store_pairs<T, V, PAIRS>(out.p[0] + z * (BWD ? minor_step : major_step), lo[e], hi[e], on_hi[e], u, v);
+      const auto write = [&](int e, const float (&u)[V], const float (&v)[V]) {
+        if (live && out.head < H && on[e]) store_pairs<T, V, PAIRS>(out.p[0], lo[e], hi[e], on_hi[e], u, v);
       };
       if (out.kind == 2) {              // v is only laid out
 #pragma unroll
-        for (int z = 0; z < R; ++z)
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if constexpr (BWD) write(z, e, ga[z][e], gb[z][e]);
-            else write(z, e, xa[z][e], xb[z][e]);
-          }
+        for (int e = 0; e < E; ++e) {
+          if constexpr (BWD) write(e, ga[e], gb[e]);
+          else write(e, xa[e], xb[e]);
+        }
         out.next(a, first, step, BWD ? minor_step : major_step, 0, target);
         continue;
       }
@@ -244,71 +280,68 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
           if constexpr (V > 1 && PAIRS == PAIRS_INTERLEAVED) deal(wa[e], wb[e]);
         }
       }
+      float r = 1.0f, back = 0.0f, ss[V] = {}, dot[V] = {}, gwa[E][V], gwb[E][V];
 #pragma unroll
-      for (int z = 0; z < R; ++z) {
-        float r = 1.0f, back = 0.0f, ss[V] = {}, dot[V] = {}, gwa[E][V], gwb[E][V];
+      for (int e = 0; e < E; ++e) {
+        fma_v<V>(ss, xa[e], xa[e], ss);
+        fma_v<V>(ss, xb[e], xb[e], ss);
+        if (BWD) {   // the rotation's transpose, then the weights
+          float u[V], v[V];
+          mul_v<V>(u, ga[e], ns[e]);
+          mul_v<V>(v, gb[e], sn[e]);
+          fma_v<V>(ga[e], ga[e], cs[e], v);
+          fma_v<V>(gb[e], gb[e], cs[e], u);
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          fma_v<V>(ss, xa[z][e], xa[z][e], ss);
-          fma_v<V>(ss, xb[z][e], xb[z][e], ss);
-          if (BWD) {   // the rotation's transpose, then the weights
-            float u[V], v[V];
-            mul_v<V>(u, ga[z][e], ns[e]);
-            mul_v<V>(v, gb[z][e], sn[e]);
-            fma_v<V>(ga[z][e], ga[z][e], cs[e], v);
-            fma_v<V>(gb[z][e], gb[z][e], cs[e], u);
+          for (int q = 0; q < V; ++q) {
+            gwa[e][q] = ga[e][q];
+            gwb[e][q] = gb[e][q];
+          }
+          if (scaled) {
+            mul_v<V>(gwa[e], ga[e], wa[e]);
+            mul_v<V>(gwb[e], gb[e], wb[e]);
+          }
+          fma_v<V>(dot, gwa[e], xa[e], dot);
+          fma_v<V>(dot, gwb[e], xb[e], dot);
+        }
+      }
+      if (a.norm != TTT_NORM_NONE) {
+        const float s = sum_v<V>(ss), d = BWD ? sum_v<V>(dot) : 0.0f;
+        r = rsqrtf(fmaf(group_sum(s, lanes), inv_h, a.eps));
+        if (BWD) back = -r * r * r * group_sum(d, lanes) * inv_h;
+      }
 #pragma unroll
-            for (int q = 0; q < V; ++q) {
-              gwa[e][q] = ga[z][e][q];
-              gwb[e][q] = gb[z][e][q];
+      for (int e = 0; e < E; ++e) {
+        float oa[V], ob[V], u[V], v[V];
+        if constexpr (!BWD) {
+          mul_v<V>(u, xa[e], r);
+          mul_v<V>(v, xb[e], r);
+          if (scaled) {
+            mul_v<V>(u, u, wa[e]);
+            mul_v<V>(v, v, wb[e]);
+          }
+          mul_v<V>(oa, v, ns[e]);
+          mul_v<V>(ob, u, sn[e]);
+          fma_v<V>(oa, u, cs[e], oa);
+          fma_v<V>(ob, v, cs[e], ob);
+        } else {
+          // dx = r (g w) - x r^3 <g w, x> [/ h];  dw += g (x r)
+          mul_v<V>(oa, xa[e], back);
+          mul_v<V>(ob, xb[e], back);
+          fma_v<V>(oa, gwa[e], r, oa);
+          fma_v<V>(ob, gwb[e], r, ob);
+          if (a.partials) {
+            mul_v<V>(u, xa[e], r);
+            mul_v<V>(v, xb[e], r);
+            if (kind == 0) {
+              fma_v<V>(dw[0][e][0], ga[e], u, dw[0][e][0]);
+              fma_v<V>(dw[0][e][1], gb[e], v, dw[0][e][1]);
+            } else {
+              fma_v<V>(dw[1][e][0], ga[e], u, dw[1][e][0]);
+              fma_v<V>(dw[1][e][1], gb[e], v, dw[1][e][1]);
             }
-            if (scaled) {
-              mul_v<V>(gwa[e], ga[z][e], wa[e]);
-              mul_v<V>(gwb[e], gb[z][e], wb[e]);
-            }
-            fma_v<V>(dot, gwa[e], xa[z][e], dot);
-            fma_v<V>(dot, gwb[e], xb[z][e], dot);
           }
         }
-        if (a.norm != TTT_NORM_NONE) {
-          const float s = sum_v<V>(ss), d = BWD ? sum_v<V>(dot) : 0.0f;
-          r = rsqrtf(fmaf(group_sum(s, lanes), inv_h, a.eps));
-          if (BWD) back = -r * r * r * group_sum(d, lanes) * inv_h;
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          float oa[V], ob[V], u[V], v[V];
-          if constexpr (!BWD) {
-            mul_v<V>(u, xa[z][e], r);
-            mul_v<V>(v, xb[z][e], r);
-            if (scaled) {
-              mul_v<V>(u, u, wa[e]);
-              mul_v<V>(v, v, wb[e]);
-            }
-            mul_v<V>(oa, v, ns[e]);
-            mul_v<V>(ob, u, sn[e]);
-            fma_v<V>(oa, u, cs[e], oa);
-            fma_v<V>(ob, v, cs[e], ob);
-          } else {
-            // dx = r (g w) - x r^3 <g w, x> [/ h];  dw += g (x r)
-            mul_v<V>(oa, xa[z][e], back);
-            mul_v<V>(ob, xb[z][e], back);
-            fma_v<V>(oa, gwa[e], r, oa);
-            fma_v<V>(ob, gwb[e], r, ob);
-            if (a.partials) {
-              mul_v<V>(u, xa[z][e], r);
-              mul_v<V>(v, xb[z][e], r);
-              if (kind == 0) {
-                fma_v<V>(dw[0][e][0], ga[z][e], u, dw[0][e][0]);
-                fma_v<V>(dw[0][e][1], gb[z][e], v, dw[0][e][1]);
-              } else {
-                fma_v<V>(dw[1][e][0], ga[z][e], u, dw[1][e][0]);
-                fma_v<V>(dw[1][e][1], gb[z][e], v, dw[1][e][1]);
-              }
-            }
-          }
-          write(z, e, oa, ob);
-        }
+        write(e, oa, ob);
       }
       out.next(a, first, step, BWD ? minor_step : major_step, 0, target);
     }
@@ -358,7 +391,9 @@ cudaError_t launch_tiles(const HeadArgs& a, int lanes, cudaStream_t s) {
   while (2 << log_tile <= groups && (M >> (log_tile + 1)) >= 148 * 4) ++log_tile;
   const long long tiles = (M + (1 << log_tile) - 1) >> log_tile;
   const long long blocks = BWD ? head_bwd_blocks(a.B, a.N) : tiles;
-  const size_t smem = BWD && a.partials ? 2 * (size_t)a.h * sizeof(float) : 0;
+  size_t smem = BWD ? (2 * (size_t)a.h * sizeof(float) + 15) / 16 * 16 : 0;
+  using L = Ring<T, V, E, BWD>;
+  if (L::on) smem += (size_t)L::depth * L::bytes * kHeadThreads;
   head_kernel<T, V, PAIRS, E, BWD><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, log_tile, lanes);
   return cudaGetLastError();
 }

@@ -127,6 +127,10 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, bool on) 
                    (unsigned)__cvta_generic_to_shared(dst)), "l"(src), "n"(BYTES), "r"(on ? BYTES : 0)
                : "memory");
 }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for all but the newest N groups of this thread's copies.
+template <int N>
+__device__ __forceinline__ void copies_wait_but() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <typename T, int V>
