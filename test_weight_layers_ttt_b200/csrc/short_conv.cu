@@ -4,8 +4,8 @@
 // HBM bound: a token costs one read and one write of its channels forward, two reads and one
 // write backward. A thread owns V consecutive channels over a run of tokens and slides the
 // window through registers, so a row is read once per run (plus width - 1 halo rows) and every
-// access of the vector form is 8 or 16 bytes. The next kAhead rows are loaded before the
-// current ones are used: bytes in flight set the rate, and the arithmetic is two-wide.
+// access of the vector form is 8 or 16 bytes. kRing rows are on their way while one is used:
+// bytes in flight set the rate; the arithmetic is two-wide.
 #include "mixer.h"
 #include "mixer_common.cuh"
 
@@ -13,7 +13,6 @@ namespace ttt {
 namespace {
 
 constexpr int kConvThreads = 128;
-constexpr int kAhead = 4;    // rows loaded together, while the rows before are used
 
 __device__ __forceinline__ int sequence_length(const int* lens, int b, int N) {
   return lens ? min(max(lens[b], 0), N) : N;
@@ -34,6 +33,37 @@ __device__ __forceinline__ void history_row(const ConvArgs& a, int b, int c, lon
   }
 }
 
+// The rows of up to two tensors on their way to a thread: kRing of them in shared memory by
+// asynchronous copies, each thread's own, where a row's access has the 4 bytes that such a copy
+// takes at least; else kRing in registers.
+#ifndef RNG
+#define RNG 4
+#endif
+constexpr int kRing = RNG;
+template <typename T, int V, int TENSORS>
+struct Rows {
+  using U = typename Pack<T, V>::U;
+  static constexpr bool shared = V * sizeof(T) >= 4;
+  U held[shared ? 1 : TENSORS][shared ? 1 : kRing];
+  U* ring;
+  __device__ __forceinline__ Rows(U* base) : ring(base + threadIdx.x) {}
+  // Entry i (a compile-time number below kRing) of tensor k from p, or zeros.
+  __device__ __forceinline__ void load(int k, int i, const T* p, bool on) {
+    if constexpr (shared) copy_async<sizeof(U)>(ring + (k * kRing + i) * kConvThreads, p, on);
+    else load_here(p, on, held[k][i]);
+  }
+  __device__ __forceinline__ void loaded() {   // the loads of one row of every tensor
+    if constexpr (shared) copies_commit();
+  }
+  __device__ __forceinline__ void wait_oldest() {
+    if constexpr (shared) copies_wait_but<kRing - 1>();
+  }
+  __device__ __forceinline__ void take(int k, int i, float (&f)[V]) {
+    if constexpr (shared) unpack<T, V>(ring[(k * kRing + i) * kConvThreads], f);
+    else unpack<T, V>(held[k][i], f);
+  }
+};
+
 // V fp32 parameters, aligned or not.
 template <int V>
 __device__ __forceinline__ void load_params(const float* p, float (&f)[V]) {
@@ -44,6 +74,7 @@ __device__ __forceinline__ void load_params(const float* p, float (&f)[V]) {
 // grid (channel blocks * runs, B): the channel blocks of one run are neighbours.
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int cblocks, int run) {
+  __shared__ __align__(16) typename Pack<T, V>::U ring[V * sizeof(T) >= 4 ? kRing * kConvThreads : 1];
   const int c = ((blockIdx.x % cblocks) * kConvThreads + threadIdx.x) * V;
   if (c >= a.D) return;
   const int b = blockIdx.y;
@@ -63,21 +94,22 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int 
 #pragma unroll
     for (int j = 1; j < K; ++j) history_row<T, V, K>(a, b, c, (long long)t0 - j + K - 1, win[j - 1]);
     const int te = min(t1, n);
-    typename Pack<T, V>::U next[kAhead];
-    const auto fetch = [&](int t) {
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) load_here(x + (long long)(t + i) * a.x_row, t + i < te, next[i]);
+    Rows<T, V, 1> rows(ring);
+    const T* ahead = x + (long long)t0 * a.x_row;
+    const auto fetch = [&](int i, int t) {
+      rows.load(0, i, ahead, t < te);
+      rows.loaded();
+      ahead += a.x_row;
     };
-    fetch(t0);
-    for (int t = t0; t < te; t += kAhead) {
-      typename Pack<T, V>::U raw[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) raw[i] = next[i];
-      fetch(t + kAhead);
+    for (int i = 0; i < kRing; ++i) fetch(i, t0 + i);
+    for (int t = t0; t < te; t += kRing) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+      for (int i = 0; i < kRing; ++i) {
         float cur[V], o[V];
-        unpack<T, V>(raw[i], cur);
+        rows.wait_oldest();
+        rows.take(0, i, cur);
+        fetch(i, t + i + kRing);
         fma_v<V>(o, w[0], cur, bias);
 #pragma unroll
         for (int j = 1; j < K; ++j) fma_v<V>(o, w[j], win[j - 1], o);
@@ -147,6 +179,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_step_kernel(ConvArgs a) {
 // of its own tokens into one row of partials, which column_sums joins in a fixed order.
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int cblocks, int run) {
+  __shared__ __align__(16) typename Pack<T, V>::U ring[V * sizeof(T) >= 4 ? 2 * kRing * kConvThreads : 1];
   const int c = ((blockIdx.x % cblocks) * kConvThreads + threadIdx.x) * V;
   if (c >= a.D) return;
   const int b = blockIdx.y;
@@ -183,33 +216,31 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
       for (int q = 0; q < V; ++q) win[j - 1][q] = 0.0f;
   }
   const int s1 = t1 + K - 1, se = min(s1, n);
-  typename Pack<T, V>::U nx[kAhead], ng[kAhead];
-  const auto fetch = [&](int s) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      load_here(x + (long long)(s + i) * a.x_row, s + i < se, nx[i]);
-      load_here(dy + (long long)(s + i) * a.D, s + i < se, ng[i]);
-    }
+  Rows<T, V, 2> rows(ring);
+  const T* ahead_x = x + (long long)t0 * a.x_row;
+  const T* ahead_g = dy + (long long)t0 * a.D;
+  const auto fetch = [&](int i, int s) {
+    rows.load(0, i, ahead_x, s < se);
+    rows.load(1, i, ahead_g, s < se);
+    rows.loaded();
+    ahead_x += a.x_row;
+    ahead_g += a.D;
   };
-  fetch(t0);
-  for (int s0 = t0; s0 < s1; s0 += kAhead) {
-    typename Pack<T, V>::U rx[kAhead], rg[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      rx[i] = nx[i];
-      rg[i] = ng[i];
-    }
-    fetch(s0 + kAhead);
+  for (int i = 0; i < kRing; ++i) fetch(i, t0 + i);
+  for (int s0 = t0; s0 < s1; s0 += kRing) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < kRing; ++i) {
       const int s = s0 + i;
       float cur[V];
 #pragma unroll
       for (int q = 0; q < V; ++q)
 #pragma unroll
         for (int j = K - 1; j > 0; --j) g[j][q] = g[j - 1][q];
-      unpack<T, V>(rx[i], cur);       // zeros behind the sequence's end
-      unpack<T, V>(rg[i], g[0]);
+      rows.wait_oldest();
+      rows.take(0, i, cur);           // zeros behind the sequence's end
+      rows.take(1, i, g[0]);
+      fetch(i, s + kRing);
       if (a.act) {
         float pre[V];
         fma_v<V>(pre, w[0], cur, bias);
