@@ -4,13 +4,18 @@
 //     y_t = sum_s C_t[s] h_t + D[d] u_t,  times silu(z_t) when gated.
 //
 // What bounds it: one exponential per (token, channel, state) - 16 per token and channel at
-// the usual S = 16 - against 16 exponentials per clock and SM; the four fp32 operations
-// around it need half that time and HBM less than that. So the work is laid out for the
-// exponential unit to run without a pause: a lane keeps a register tile of 2 channels x 4
-// states (8 independent recurrences, the channel pair packed for the two-wide fp32
-// instructions, which halves the issue slots), SL lanes share a channel's states, and tiles of
-// tokens are staged in shared memory as fp32 with softplus already applied. The sums over the
-// states leave a warp by transposing butterflies (SL values over SL lanes in SL - 1 shuffles).
+// the usual S = 16 - against 16 exponentials per clock and SM (measured; the fp32 pipe does 125
+// operations, two-wide or not). That is 231 us for 8 x 2048 tokens of 4096 channels, where HBM
+// needs 82 us. The kernel takes 447 us: the exponential unit is busy 61 % of it, the shared
+// memory pipe 69 %, the schedulers 58 %, so what is left is their overlap.
+//
+// Layout: a lane keeps 4 states of one channel (2 channels in the backward) in registers, packed
+// in pairs for the two-wide fp32 instructions, which halves the issue slots; SL lanes share a
+// channel's states; tiles of tokens are staged in shared memory as fp32 with softplus already
+// applied, the next tile's operands on their way meanwhile. 8 states a lane (half the lanes,
+// less shared memory traffic) took 568 us against 519 us at the time: too few warps. Each
+// lane's part of a sum over states goes through shared memory to the threads that write the
+// results (a transposing shuffle took 6 more instructions per token).
 //
 // The time axis is cut into chunks when batch x channels alone would leave SMs idle: a first
 // pass takes each chunk's end state from zero (its decay is exp(A sum delta), one number per
@@ -506,10 +511,13 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
 //     du_t = D g_t + delta_t x_t,  ddelta_t = sum_s A p_t + u_t x_t,
 //     dz_t = dy_t silu'(z_t) (sum_s C_t h_t + D u_t).
 // The states are recomputed, not saved: the first pass leaves a mark (the state from the
-// chunk's zero) every 8 tokens, the main pass walks the marks backwards and holds 8 tokens of
-// a_t and h_t in registers, so each a_t is computed twice in all. 8 tokens: the marks then cost
-// S / 8 * 4 bytes per token and channel (8 at S = 16, less than the operands), and 8 tokens of
-// (a, h) fill the 128 registers that two blocks per SM leave.
+// chunk's zero) every 8 tokens and the main pass walks the marks backwards. Marks of 8 tokens
+// cost S / 8 * 4 bytes per token and channel (8 at S = 16, less than the operands), and their
+// states recomputed are as many as registers hold. Some 25 fp32 operations per state, 2.5
+// exponentials and 15 shuffles, shared memory and scheduler cycles around them: at 4 x 4096
+// tokens of 2048 channels 985 us (260 us marks, 690 us main pass, 35 us joins and sums) against
+// 115 us of exponentials and some 290 us of fp32 operations; the main pass issues 52 % of the
+// time with the 12 warps per SM that its registers leave.
 
 // Marks, chunk end states, and with more than one chunk the chunk's share of the state gradient
 // in front of it, sum_t (prod_{t' <= t} a_t') C_t g_t. Same tiling as the forward.
@@ -692,8 +700,10 @@ __device__ __forceinline__ int mark_slot(int ch, int sl) {
 // The main pass of one chunk, 8 tokens at a time from its end. grid (channel blocks, chunks, B).
 // Of the 8 tokens only 4 at a time hold their a_t and h_t in registers: the first 4 are run
 // through once for the state in front of the last 4, and again when their turn comes. That is
-// half an exponential more per state, and three blocks per SM instead of two.
-// VEC: the next 8 tokens' operands come by asynchronous copies under this one's arithmetic.
+// half an exponential more per state, and three blocks per SM instead of two (1251 us against
+// 1322 us at the time, both sides without spills). A token's operands are read, and its channel
+// sums shuffled, a token apart from their use (756 -> 698 us). VEC: the next 8 tokens' operands
+// come by asynchronous copies under this one's arithmetic; else through registers, two blocks.
 template <typename T, int SL, bool VEC>
 __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArgs a, int blocks_per_group,
                                                                          bool vec_b, bool vec_c) {
@@ -1242,8 +1252,10 @@ int scan_channel_blocks(int D, int G, int S) {
 }
 
 // Blocks that run at a time (148 SMs x 7 forward, x 3 backward), and the tokens' worth of work
-// that starting and joining a chunk costs. The forward's first pass doubles its exponentials,
-// so a sequence is cut for it only where whole sequences would leave most SMs idle.
+// that starting and joining a chunk costs (8, 24 and 40 gave the same times, 64 fewer and worse
+// balanced chunks: 1203 us against 1100 us for the backward above, at the time). The forward's
+// first pass doubles its exponentials, so a sequence is cut for it only where whole sequences
+// would leave most SMs idle.
 constexpr long long kFwdSlots = 148 * 7, kBwdSlots = 148 * 3, kChunkCost = 24;
 
 int scan_chunks(int B, int N, int D, int G, int S, bool backward, int* chunk) {

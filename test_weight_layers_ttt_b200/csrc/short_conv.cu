@@ -5,7 +5,10 @@
 // write backward. A thread owns V consecutive channels over a run of tokens and slides the
 // window through registers, so a row is read once per run (plus width - 1 halo rows) and every
 // access of the vector form is 8 or 16 bytes. kRing rows are on their way while one is used:
-// bytes in flight set the rate; the arithmetic is two-wide.
+// bytes in flight set the rate (2 rows 74 us, 4 rows 58 us, 8 rows 56 us forward and 74 us
+// against 70 us backward); the arithmetic is two-wide. 2 x 32768 tokens of 1024 channels, width
+// 4, silu, bf16: 58 us forward, 4.6 TB/s; the exponential unit, two results per silu, is busy 58 %
+// of it. 4 x 4096 tokens of 2048 channels backward: 70 us, 61 % of the issue slots.
 #include "mixer.h"
 #include "mixer_common.cuh"
 
@@ -36,10 +39,7 @@ __device__ __forceinline__ void history_row(const ConvArgs& a, int b, int c, lon
 // The rows of up to two tensors on their way to a thread: kRing of them in shared memory by
 // asynchronous copies, each thread's own, where a row's access has the 4 bytes that such a copy
 // takes at least; else kRing in registers.
-#ifndef RNG
-#define RNG 4
-#endif
-constexpr int kRing = RNG;
+constexpr int kRing = 4;
 template <typename T, int V, int TENSORS>
 struct Rows {
   using U = typename Pack<T, V>::U;
