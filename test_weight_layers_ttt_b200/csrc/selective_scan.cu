@@ -12,8 +12,9 @@
 // Layout: a lane keeps 4 states of one channel (2 channels in the backward) in registers, packed
 // in pairs for the two-wide fp32 instructions, which halves the issue slots; SL lanes share a
 // channel's states; tiles of tokens are staged in shared memory as fp32 with softplus already
-// applied, the next tile's operands on their way meanwhile. 8 states a lane (half the lanes,
-// less shared memory traffic) took 568 us against 519 us at the time: too few warps. Each
+// applied, the next tile's operands on their way meanwhile. Larger register tiles have fewer
+// instructions and less shared memory traffic, but too few warps: 8 states a lane took 568 us
+// against 519 us at the time, 2 channels x 4 states 523 us against 447 us. Each
 // lane's part of a sum over states goes through shared memory to the threads that write the
 // results (a transposing shuffle took 6 more instructions per token).
 //
