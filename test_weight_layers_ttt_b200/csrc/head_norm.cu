@@ -189,29 +189,31 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
     out.enter(a, 0, first, target);
     RawPairs<T, V> rx[E], rg[E];
     int put = 0, take = 0;              // ring entries
-    const auto fetch = [&]() {
+    const auto fetch = [&]() {          // behind the last row nothing is loaded, nor waited for
       const bool row = in.kind < 3 && live && in.head < a.H[in.kind < 3 ? in.kind : 0];
+      if (in.kind < 3) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const bool x = row && (!BWD || in.kind < 2);
-        if constexpr (RING) {
-          U* q = ring + (put * ITEMS + e * (BWD ? 4 : 2)) * kHeadThreads;
-          copy_async<sizeof(U)>(q, in.p[0] + lo[e], x && on[e]);
-          copy_async<sizeof(U)>(q + kHeadThreads, in.p[0] + hi[e], x && on_hi[e]);
-          if (BWD) {
-            copy_async<sizeof(U)>(q + 2 * kHeadThreads, in.p[1] + lo[e], row && on[e]);
-            copy_async<sizeof(U)>(q + 3 * kHeadThreads, in.p[1] + hi[e], row && on_hi[e]);
+        for (int e = 0; e < E; ++e) {
+          const bool x = row && (!BWD || in.kind < 2);
+          if constexpr (RING) {
+            U* q = ring + (put * ITEMS + e * (BWD ? 4 : 2)) * kHeadThreads;
+            copy_async<sizeof(U)>(q, in.p[0] + lo[e], x && on[e]);
+            copy_async<sizeof(U)>(q + kHeadThreads, in.p[0] + hi[e], x && on_hi[e]);
+            if (BWD) {
+              copy_async<sizeof(U)>(q + 2 * kHeadThreads, in.p[1] + lo[e], row && on[e]);
+              copy_async<sizeof(U)>(q + 3 * kHeadThreads, in.p[1] + hi[e], row && on_hi[e]);
+            }
+          } else {
+            load_raw_pairs<T, V>(rx[e], in.p[0], lo[e], hi[e], x && on[e], x && on_hi[e]);
+            if (BWD) load_raw_pairs<T, V>(rg[e], in.p[1], lo[e], hi[e], row && on[e], row && on_hi[e]);
           }
-        } else {
-          load_raw_pairs<T, V>(rx[e], in.p[0], lo[e], hi[e], x && on[e], x && on_hi[e]);
-          if (BWD) load_raw_pairs<T, V>(rg[e], in.p[1], lo[e], hi[e], row && on[e], row && on_hi[e]);
         }
+        in.next(a, first, step, minor_step, BWD ? major_step : 0, source);
       }
       if constexpr (RING) {
         copies_commit();
         put = put + 1 == DEPTH ? 0 : put + 1;
       }
-      if (in.kind < 3) in.next(a, first, step, minor_step, BWD ? major_step : 0, source);
     };
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) fetch();

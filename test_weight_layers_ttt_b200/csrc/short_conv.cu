@@ -58,6 +58,9 @@ struct Rows {
   __device__ __forceinline__ void wait_oldest() {
     if constexpr (shared) copies_wait_but<kRing - 1>();
   }
+  __device__ __forceinline__ void drain() {    // no copy outlives its thread
+    if constexpr (shared) copies_wait();
+  }
   __device__ __forceinline__ void take(int k, int i, float (&f)[V]) {
     if constexpr (shared) unpack<T, V>(ring[(k * kRing + i) * kConvThreads], f);
     else unpack<T, V>(held[k][i], f);
@@ -126,6 +129,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_fwd_kernel(ConvArgs a, int 
         }
       }
     }
+    rows.drain();
   }
   // rows behind the sequence's end
   const float zero[V] = {};
@@ -287,6 +291,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
       }
     }
   }
+  rows.drain();
   float* part = a.partials + ((long long)b * runs + r) * (K + 1) * a.D + c;
 #pragma unroll
   for (int q = 0; q < V; ++q) {

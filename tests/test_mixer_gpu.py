@@ -388,6 +388,48 @@ def test_padded_sequences_equal_their_own_calls(n):
     assert float(y[0, n:].abs().max()) == 0.0 if n < 300 else True
 
 
+def test_a_step_of_zero_keeps_the_state_exactly():
+    """delta = 0 decays by exp(0) = 1 and adds nothing, in the prompt, its pieces and a token."""
+    h, g, _ = scan_case("fp32", 2, 600, 24, 16, 1, False, True, None, False, 0, seed=23)
+    g["dt"].zero_()
+    g["dt_bias"].zero_()
+    before = g["state"].clone()
+    _, st = layer.selective_scan_fwd(**g)
+    assert torch.equal(st, before)
+    one = {k: v[:, 0].contiguous() if k in ("u", "dt", "Bm", "Cm") else v for k, v in g.items()}
+    layer.selective_scan_step(**one)
+    assert torch.equal(g["state"], before)
+    ds = torch.randn_like(before)
+    got = layer.selective_scan_bwd(**g, dy=torch.zeros_like(g["u"]), dstate=ds)
+    assert torch.equal(got[8], ds)
+
+
+def test_nan_and_inf_stay_where_they_belong():
+    h, g, _ = scan_case("fp32", 2, 300, 70, 16, 1, True, True, None, True, 0, seed=25)
+    y, st = layer.selective_scan_fwd(**g)
+    bad = {**g, "u": g["u"].clone()}
+    bad["u"][1, 100, 33] = float("nan")
+    y2, st2 = layer.selective_scan_fwd(**bad)
+    assert torch.isnan(y2[1, 100:, 33]).all() and torch.isnan(st2[1, 33]).all()
+    y2[1, 100:, 33], st2[1, 33] = y[1, 100:, 33], st[1, 33]
+    assert torch.equal(y, y2) and torch.equal(st, st2)
+    x, w, bias, _, xg, wg, c, _ = conv_case("bf16", 1, 40, 24, 4, "silu", False, None, 0, seed=26)
+    y, _ = layer.short_conv_fwd(xg, wg, **c)
+    xg[0, 20, 5] = float("inf")
+    y2, _ = layer.short_conv_fwd(xg, wg, **c)
+    ref = torch.nn.functional.silu(torch.where(wg[:, 5] > 0, float("inf"), -float("inf")))   # taps in turn
+    assert torch.equal(torch.isnan(y2[0, 20:24, 5]), torch.isnan(ref)) and torch.isinf(y2[0, 20:24, 5]).equal(torch.isinf(ref))
+    y2[0, 20:24, 5] = y[0, 20:24, 5]
+    assert torch.equal(y, y2)
+    q = torch.randn((2, 5, 3, 64), device="cuda")
+    o, _, _ = layer.head_norm_rope_fwd(q, None, None)
+    q[1, 2, 1, 7] = float("nan")
+    o2, _, _ = layer.head_norm_rope_fwd(q, None, None)
+    assert torch.isnan(o2[1, 1, 2]).all()
+    o2[1, 1, 2] = o[1, 1, 2]
+    assert torch.equal(o, o2)
+
+
 # ----------------------------------------------------------------------------- how they are called
 def together(g):
     """Projection -> short convolution -> heads -> the layer's linear attention and, beside it,
