@@ -10,10 +10,13 @@
 
 namespace ttt {
 
-// out[c] = sum over r of part[r, c] for C columns (out0 takes the first n0 columns, out1 the
-// rest; either may be null), rows in a fixed order.
-cudaError_t column_sums(const float* part, long long R, long long C, float* out0, long long n0,
-                        float* out1, cudaStream_t s);
+// out[c] = sum over r of part[r, c], rows in a fixed order, for the n0 + n1 + n2 columns of three
+// outputs side by side (each may be null).
+struct SumOuts {
+  float* p[3];
+  long long n[3];
+};
+cudaError_t column_sums(const float* part, long long R, const SumOuts& outs, cudaStream_t s);
 
 // ------------------------------------------------------------------ short convolution
 struct ConvArgs {
@@ -88,8 +91,7 @@ struct ScanArgs {
   float* back;    // [B, chunks, D, SP]: a chunk's share of the state gradient before it, then
                   // the state gradient behind each chunk
   float* bcpart;  // [channel blocks of a group, B, N, G, 2, SP]: partial dB and dC
-  float* apart;   // [B, chunks, D, S]: partial dA
-  float* dpart;   // [B, chunks, 2, D]: partial dD and ddt_bias
+  float* part;    // [B, chunks, D S + 2 D]: partial dA, dD and ddt_bias
 };
 
 constexpr int kScanSub = 8;            // tokens between two marks of the backward

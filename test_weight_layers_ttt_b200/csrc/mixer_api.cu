@@ -166,8 +166,7 @@ size_t plan_scan_bwd(ScanArgs& a, void* base) {
   a.marks = cv.take_n<float>(subs * a.D * SP);
   a.msum = cv.take_n<float>(subs * a.D);
   a.bcpart = cv.take_n<float>((long long)scan_channel_blocks(a.D, a.G, a.S) * a.B * a.N * a.G * 2 * SP);
-  a.apart = cv.take_n<float>(bk * a.D * a.S);
-  a.dpart = cv.take_n<float>(bk * 2 * a.D);
+  a.part = cv.take_n<float>(bk * a.D * (a.S + 2));
   return cv.off;
 }
 
@@ -271,8 +270,8 @@ ttt_status ttt_short_conv_bwd(const ttt_conv_desc* desc, const void* x, const fl
   return with_checks(s, {{dx, rows * a.D, dt}, {dw, taps, DT_F32}, {dbias, a.D, DT_F32},
                          {dstate_in, st, dt}}, [&]() -> ttt_status {
     if (a.B > 0) TTT_OP("short_conv_bwd", conv_bwd(dt, a, s));
-    TTT_OP("short_conv_bwd_sum", column_sums(part, conv_bwd_rows(a.B, a.N, a.D),
-                                             (long long)(a.width + 1) * a.D, dw, taps, dbias, s));
+    TTT_OP("short_conv_bwd_sum",
+           column_sums(part, conv_bwd_rows(a.B, a.N, a.D), {{dw, dbias, nullptr}, {taps, a.D, 0}}, s));
     return TTT_OK;
   });
 }
@@ -371,7 +370,7 @@ ttt_status ttt_head_norm_rope_bwd(const ttt_heads_desc* desc, const void* q, con
     if (any) TTT_OP("head_norm_rope_bwd", head_bwd(dt, a, s));
     if (sums)
       TTT_OP("head_norm_rope_bwd_sum", column_sums(part, any ? head_bwd_blocks(a.B, a.N) : 0,
-                                                   2LL * a.h, dwq, a.h, dwk, s));
+                                                   {{dwq, dwk, nullptr}, {a.h, a.h, 0}}, s));
     return TTT_OK;
   });
 }
@@ -514,14 +513,12 @@ ttt_status ttt_selective_scan_bwd(const ttt_scan_desc* desc, const void* u, cons
     const long long bk = (long long)a.B * a.chunks;
     if (a.B > 0) {
       TTT_OP("selective_scan_marks", scan_bwd_marks(tag, a, s));
-      TTT_OP("selective_scan_join", scan_join(a, true, s));
+      if (a.chunks > 1) TTT_OP("selective_scan_join", scan_join(a, true, s));
       TTT_OP("selective_scan_bwd", scan_bwd_main(tag, a, s));
       if (a.N > 0) TTT_OP("selective_scan_sum_bc", scan_bwd_sum_bc(tag, a, s));
     }
-    TTT_OP("selective_scan_sum_a", column_sums(a.apart, bk, (long long)a.D * a.S, dA, (long long)a.D * a.S,
-                                               nullptr, s));
-    if (dD || ddt_bias)
-      TTT_OP("selective_scan_sum_d", column_sums(a.dpart, bk, 2LL * a.D, dD, a.D, ddt_bias, s));
+    TTT_OP("selective_scan_sum_ad",
+           column_sums(a.part, bk, {{dA, dD, ddt_bias}, {(long long)a.D * a.S, a.D, a.D}}, s));
     return TTT_OK;
   });
 }

@@ -640,9 +640,11 @@ __global__ void __launch_bounds__(kFwdThreads) scan_marks_kernel(ScanArgs a, int
     __syncthreads();
   }
   const long long at = ((long long)b * a.chunks + chunk) * a.D + c;
-  store_states(a.ends + at * SP, h);
-  if (SPLIT) store_states(a.back + at * SP, share);
-  if (sl == 0 && mine) a.dsum[at] = dsum;
+  if (SPLIT) {
+    store_states(a.ends + at * SP, h);
+    store_states(a.back + at * SP, share);
+    if (sl == 0 && mine) a.dsum[at] = dsum;
+  }
 }
 
 // The main pass's tile: a lane holds 2 channels x 4 states (8 recurrences, so that the sums
@@ -730,16 +732,22 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
 #pragma unroll
   for (int z = 0; z < 2; ++z) {
     float w[4] = {}, g[4] = {}, v[4];
-    if (c + z < r.c1) {
+    if (c + z < r.c1 && a.chunks > 1) {
       load_vec<float, 4>(a.ends + (bk * a.D + c + z) * SP + sl * 4, w);
       load_vec<float, 4>(a.back + (bk * a.D + c + z) * SP + sl * 4, g);
     }
-    sm.start[z * kThreads + threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int s = sl * 4 + i;
-      v[i] = c + z < r.c1 && s < a.S ? a.A[(long long)(c + z) * a.S + s] * kLog2e : 0.0f;
+      const bool on = c + z < r.c1 && s < a.S;
+      const long long io = ((long long)b * a.D + c + z) * a.S + s;
+      v[i] = on ? a.A[(long long)(c + z) * a.S + s] * kLog2e : 0.0f;
+      if (on && a.chunks == 1) {        // one piece: nothing was joined
+        w[i] = a.state_in ? a.state_in[io] : 0.0f;
+        g[i] = a.dstate_out ? a.dstate_out[io] : 0.0f;
+      }
     }
+    sm.start[z * kThreads + threadIdx.x] = make_float4(w[0], w[1], w[2], w[3]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       carry[z][i] = pack2(g[2 * i], g[2 * i + 1]);
@@ -1118,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
       for (int q = 0; q < 2; ++q) {
         const int s = sl * 4 + 2 * i + q;
         if (c + z >= r.c1 || s >= a.S) continue;
-        a.apart[(bk * a.D + c + z) * a.S + s] = w[q];
+        a.part[bk * a.D * (a.S + 2) + (long long)(c + z) * a.S + s] = w[q];
         if (a.dstate_in && chunk == 0) a.dstate_in[((long long)b * a.D + c + z) * a.S + s] = g[q];
       }
     }
@@ -1129,21 +1137,29 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) v += sm.acc[which][k * CB + ch];
-    if (r.c0 + ch < r.c1) a.dpart[(bk * 2 + which) * a.D + r.c0 + ch] = v;
+    if (r.c0 + ch < r.c1) a.part[bk * a.D * (a.S + 2) + (long long)a.D * (a.S + which) + r.c0 + ch] = v;
   }
 }
 
-// dB and dC: the sum over the channel blocks of a group, rounded once.
+// dB and dC: the sum over the channel blocks of a group, rounded once. Four states a thread.
 template <typename T>
 __global__ void __launch_bounds__(256) scan_sum_bc_kernel(ScanArgs a, int blocks_per_group, int SP) {
-  const long long rows = (long long)a.B * a.N * a.G;
-  TTT_GRID_LOOP(i, rows * 2 * SP) {
-    const int q = (int)(i % (2 * SP)), s = q % SP;
-    const long long row = i / (2 * SP);
-    if (s >= a.S) continue;
-    float v = 0.0f;
-    for (int k = 0; k < blocks_per_group; ++k) v += a.bcpart[k * rows * 2 * SP + i];
-    static_cast<T*>(q < SP ? a.dB : a.dC)[row * a.S + s] = from_f32<T>(v);
+  const long long n = (long long)a.B * a.N * a.G * 2 * SP;   // of one channel block
+  TTT_GRID_LOOP(i, n / 4) {
+    const int q = (int)(i * 4 % (2 * SP)), s = q % SP;
+    const long long row = i * 4 / (2 * SP);
+    float v[4] = {};
+#pragma unroll 8
+    for (int k = 0; k < blocks_per_group; ++k) {
+      float f[4];
+      load_vec<float, 4>(a.bcpart + k * n + i * 4, f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] += f[e];
+    }
+    T* out = static_cast<T*>(q < SP ? a.dB : a.dC) + row * a.S;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (s + e < a.S) out[s + e] = from_f32<T>(v[e]);
   }
 }
 
@@ -1301,7 +1317,7 @@ cudaError_t scan_step(int dt, const ScanArgs& a, cudaStream_t s) {
 
 cudaError_t scan_bwd_sum_bc(int dt, const ScanArgs& a, cudaStream_t s) {
   const int SP = scan_padded_state(a.S), bpg = scan_channel_blocks(a.D, a.G, a.S);
-  const unsigned grid = grid_for((long long)a.B * a.N * a.G * 2 * SP, 256);
+  const unsigned grid = grid_for((long long)a.B * a.N * a.G * 2 * SP / 4, 256);
   if (dt == DT_BF16) scan_sum_bc_kernel<bf16><<<grid, 256, 0, s>>>(a, bpg, SP);
   else scan_sum_bc_kernel<float><<<grid, 256, 0, s>>>(a, bpg, SP);
   return cudaGetLastError();

@@ -304,9 +304,9 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
 // 32 columns x 16 row groups per block; row group g adds rows g, g + 16, ... in order.
 constexpr int kSumRows = 16;
 __global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const float* part, long long R, long long C,
-                                                                    float* out0, long long n0, float* out1) {
+                                                                    SumOuts outs) {
   __shared__ float acc[kSumRows][33];
-  const long long c = (long long)blockIdx.x * 32 + threadIdx.x;
+  long long c = (long long)blockIdx.x * 32 + threadIdx.x;
   float v = 0.0f;
   if (c < C) {
 #pragma unroll 8
@@ -317,10 +317,10 @@ __global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const float*
   if (threadIdx.y == 0 && c < C) {
 #pragma unroll
     for (int g = 1; g < kSumRows; ++g) v += acc[g][threadIdx.x];
-    if (c < n0) {
-      if (out0) out0[c] = v;
-    } else if (out1) {
-      out1[c - n0] = v;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      if (c >= 0 && c < outs.n[k] && outs.p[k]) outs.p[k][c] = v;
+      c -= outs.n[k];
     }
   }
 }
@@ -394,9 +394,9 @@ cudaError_t launch(int dt, const ConvArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t column_sums(const float* part, long long R, long long C, float* out0, long long n0,
-                        float* out1, cudaStream_t s) {
-  column_sums_kernel<<<(unsigned)((C + 31) / 32), dim3(32, kSumRows), 0, s>>>(part, R, C, out0, n0, out1);
+cudaError_t column_sums(const float* part, long long R, const SumOuts& outs, cudaStream_t s) {
+  const long long C = outs.n[0] + outs.n[1] + outs.n[2];
+  column_sums_kernel<<<(unsigned)((C + 31) / 32), dim3(32, kSumRows), 0, s>>>(part, R, C, outs);
   return cudaGetLastError();
 }
 
