@@ -1279,7 +1279,7 @@ int scan_chunks(int B, int N, int D, int G, int S, bool backward, int* chunk) {
   const int CB = backward ? kWarps * 64 / state_lanes(S) : kFwdWarps * 32 / state_lanes(S);
   const long long blocks = (long long)B * G * ((D / G + CB - 1) / CB);
   const long long slots = backward ? kBwdSlots : kFwdSlots;
-  const long long most = std::min<long long>(std::max(1, N / 64), 1024);
+  const long long most = std::min<long long>(std::max(1, (N + 31) / 32), 1024);
   // rounds of blocks x (tokens of a chunk + cost of a chunk), the least over the counts
   long long best = 1, least = 0;
   for (long long n = 1; n <= most; ++n) {
