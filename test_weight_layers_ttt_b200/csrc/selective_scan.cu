@@ -379,50 +379,40 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanArgs a, int b
 }
 
 // Carries states over the chunks, in place: ends[k] becomes the state chunk k starts from, and
-// in the backward back[k] the state gradient behind chunk k. One thread per (b, d, s).
+// in the backward back[k] the state gradient behind chunk k. One thread per (b, d, s) and
+// direction; eight chunks' loads at a time, for the recurrence itself is short, its loads are not.
 template <bool BWD>
 __global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs a, int SP) {
-  TTT_GRID_LOOP(i, (long long)a.B * a.D * SP) {
+  constexpr int U = 8;
+  const long long n = (long long)a.B * a.D * SP;
+  TTT_GRID_LOOP(item, BWD ? 2 * n : n) {
+    const bool back = BWD && item >= n;
+    const long long i = back ? item - n : item;
     const int s = (int)(i % SP);
     const long long bd = i / SP;
     const int d = (int)(bd % a.D), b = (int)(bd / a.D);
     const bool on = s < a.S;
     const float A2 = on ? a.A[(long long)d * a.S + s] * kLog2e : 0.0f;
-    const long long io = bd * a.S + s;
-    // four chunks' loads at a time: the recurrence itself is short, its loads are not
+    const float* first = back ? a.dstate_out : a.state_in;
+    float* io = back ? a.back : a.ends;
+    float h = on && first ? first[bd * a.S + s] : 0.0f;
+    const int last = a.chunks - 1;
     const long long bk = (long long)b * a.chunks;
-    const auto entry = [&](int k) { return ((bk + k) * a.D + d) * SP + s; };
-    float h = on && a.state_in ? a.state_in[io] : 0.0f;
-    for (int k0 = 0; k0 < a.chunks; k0 += 4) {
-      float end[4], sum[4];
+    // step j of the walk is chunk j forward, chunk last - j backward
+    const auto chunk = [&](int j) { return bk + (back ? last - j : j); };
+    for (int j0 = 0; j0 <= last; j0 += U) {
+      float end[U], sum[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = k0 + j + 1 < a.chunks;   // the last chunk's end is nobody's start
-        end[j] = in ? a.ends[entry(k0 + j)] : 0.0f;
-        sum[j] = in ? a.dsum[(bk + k0 + j) * a.D + d] : 0.0f;
+      for (int j = 0; j < U; ++j) {
+        const bool in = j0 + j < last;   // the walk's last chunk passes nothing on
+        end[j] = in ? io[(chunk(j0 + j) * a.D + d) * SP + s] : 0.0f;
+        sum[j] = in ? a.dsum[chunk(j0 + j) * a.D + d] : 0.0f;
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k0 + j >= a.chunks) break;
-        a.ends[entry(k0 + j)] = h;
+      for (int j = 0; j < U; ++j) {
+        if (j0 + j > last) break;
+        io[(chunk(j0 + j) * a.D + d) * SP + s] = h;
         h = fmaf(ex2(A2 * sum[j]), h, end[j]);
-      }
-    }
-    if (!BWD) continue;
-    float g = on && a.dstate_out ? a.dstate_out[io] : 0.0f;
-    for (int k0 = a.chunks - 1; k0 >= 0; k0 -= 4) {
-      float share[4], sum[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = k0 - j > 0;
-        share[j] = in ? a.back[entry(k0 - j)] : 0.0f;
-        sum[j] = in ? a.dsum[(bk + k0 - j) * a.D + d] : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (k0 - j < 0) break;
-        a.back[entry(k0 - j)] = g;
-        g = fmaf(ex2(A2 * sum[j]), g, share[j]);
       }
     }
   }
@@ -1305,7 +1295,7 @@ cudaError_t scan_bwd_main(int dt, const ScanArgs& a, cudaStream_t s) { return la
 
 cudaError_t scan_join(const ScanArgs& a, bool backward, cudaStream_t s) {
   const int SP = scan_padded_state(a.S);
-  const unsigned grid = grid_for((long long)a.B * a.D * SP, 256);
+  const unsigned grid = grid_for((long long)a.B * a.D * SP * (backward ? 2 : 1), 256);
   if (backward) scan_join_kernel<true><<<grid, 256, 0, s>>>(a, SP);
   else scan_join_kernel<false><<<grid, 256, 0, s>>>(a, SP);
   return cudaGetLastError();
