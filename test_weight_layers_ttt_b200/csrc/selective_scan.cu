@@ -694,7 +694,8 @@ __device__ __forceinline__ int mark_slot(int ch, int sl) {
 // Of the 8 tokens only 4 at a time hold their a_t and h_t in registers: the first 4 are run
 // through once for the state in front of the last 4, and again when their turn comes. That is
 // half an exponential more per state, and three blocks per SM instead of two (1251 us against
-// 1322 us at the time, both sides without spills). A token's operands are read, and its channel
+// 1322 us at the time, both sides without spills; 2 tokens at a time, four blocks and 1.75
+// exponentials 702 to 753 us against 700 us). A token's operands are read, and its channel
 // sums shuffled, a token apart from their use (756 -> 698 us). VEC: the next 8 tokens' operands
 // come by asynchronous copies under this one's arithmetic; else through registers, two blocks.
 template <typename T, int SL, bool VEC>
