@@ -7,8 +7,8 @@
 // access of the vector form is 8 or 16 bytes. kRing rows are on their way while one is used:
 // bytes in flight set the rate (2 rows 74 us, 4 rows 58 us, 8 rows 56 us forward and 74 us
 // against 70 us backward); the arithmetic is two-wide. 2 x 32768 tokens of 1024 channels, width
-// 4, silu, bf16: 58 us forward, 4.6 TB/s; the exponential unit, two results per silu, is busy 58 %
-// of it. 4 x 4096 tokens of 2048 channels backward: 70 us, 61 % of the issue slots.
+// 4, silu, bf16: 60 us forward, 4.5 TB/s; the exponential unit, two results per silu, is busy 58 %
+// of it. 4 x 4096 tokens of 2048 channels backward: 63 us, 61 % of the issue slots.
 #include "mixer.h"
 #include "mixer_common.cuh"
 
@@ -326,11 +326,14 @@ __global__ void __launch_bounds__(32 * kSumRows) column_sums_kernel(const float*
 }
 
 // Tokens of one thread's run. Long runs re-read less halo (width - 1 rows per run); short
-// ones give small problems enough threads: at least some 1000 per SM while the run is over 8.
-int conv_run(int B, int N, int D, int V) {
+// ones give small problems enough threads: `enough` per SM while the run is over 8. 512 forward
+// and 256 backward, whose runs re-read at both ends (2 x 8192 tokens of 1024 channels in bf16:
+// 19 us against 24 us forward and 37 us against 48 us backward with 1024).
+constexpr int kFwdEnough = 512, kBwdEnough = 256;
+int conv_run(int B, int N, int D, int V, int enough) {
   const long long groups = (long long)B * ((D + V - 1) / V);
   int run = 64;
-  while (run > 8 && groups * ((N + run - 1) / run) < 148LL * 1024) run /= 2;
+  while (run > 8 && groups * ((N + run - 1) / run) < 148LL * enough) run /= 2;
   return run;
 }
 
@@ -350,7 +353,7 @@ cudaError_t launch_width(const ConvArgs& a, cudaStream_t s) {
   if constexpr (P == STEP) {
     conv_step_kernel<T, V, K><<<dim3(cblocks, a.B), kConvThreads, 0, s>>>(a);
   } else {
-    const int run = conv_run(a.B, a.N, a.D, P == BWD ? kBwdVec : V);
+    const int run = P == BWD ? conv_run(a.B, a.N, a.D, kBwdVec, kBwdEnough) : conv_run(a.B, a.N, a.D, V, kFwdEnough);
     const int runs = a.N > 0 ? (a.N + run - 1) / run : 1;
     const dim3 grid((unsigned)((long long)cblocks * runs), a.B);
     if constexpr (P == FWD)
@@ -405,7 +408,7 @@ cudaError_t conv_step(int dt, const ConvArgs& a, cudaStream_t s) { return launch
 cudaError_t conv_bwd(int dt, const ConvArgs& a, cudaStream_t s) { return launch<BWD>(dt, a, s); }
 
 long long conv_bwd_rows(int B, int N, int D) {
-  const int run = conv_run(B, N, D, kBwdVec);
+  const int run = conv_run(B, N, D, kBwdVec, kBwdEnough);
   return (long long)B * (N > 0 ? (N + run - 1) / run : 1);
 }
 
