@@ -1259,12 +1259,14 @@ int scan_channel_blocks(int D, int G, int S) {
   return (D / G + CB - 1) / CB;
 }
 
-// Blocks that run at a time (148 SMs x 7 forward, x 3 backward), and the tokens' worth of work
-// that starting and joining a chunk costs (8, 24 and 40 gave the same times, 64 fewer and worse
-// balanced chunks: 1203 us against 1100 us for the backward above, at the time). The forward's
+// Blocks to fill the card with: two rounds of those that run at a time (148 SMs x 7 forward, x 3
+// backward; one round: 400 us against 387 us forward for 32768 tokens of 1024 channels, 990 us
+// against 980 us backward for the sizes above, three rounds 394 us and 990 us), and the tokens'
+// worth of work that starting and joining a chunk costs (8, 24 and 40 gave the same times; 64
+// fewer and worse balanced chunks, 1203 us against 1100 us backward at the time). The forward's
 // first pass doubles its exponentials, so a sequence is cut for it only where whole sequences
 // would leave most SMs idle.
-constexpr long long kFwdSlots = 148 * 7, kBwdSlots = 148 * 3, kChunkCost = 24;
+constexpr long long kFwdSlots = 148 * 14, kBwdSlots = 148 * 6, kChunkCost = 24;
 
 int scan_chunks(int B, int N, int D, int G, int S, bool backward, int* chunk) {
   const int CB = backward ? kWarps * 64 / state_lanes(S) : kFwdWarps * 32 / state_lanes(S);
