@@ -12,6 +12,8 @@
 // 64-bit product (fp32 loses far positions: 1e6 * 2^-24 is 0.06 of a radian) reduced to
 // [-1/2, 1/2] turns. 2 x 32768 tokens of 3 x 4 heads of 256: 138 us, 5.8 TB/s, 89 % of the
 // measured copy rate; 65536 tokens of 3 x 8 heads of 128 backward: 223 us, 74 %.
+#include <algorithm>
+
 #include "mixer.h"
 #include "mixer_common.cuh"
 
@@ -24,6 +26,11 @@ constexpr int kHeadThreads = 128;
 // head: 162 us with one row ahead in registers, 145 us with 4 blocks of 4 rows, 137 us with 6 of
 // 3; backward at 128: 320 us in registers, 224 us with 3 blocks of 3, 308 us with 4 blocks (spills).
 constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
+// Rows that take narrow accesses have no ring and little in flight per thread; one or two pairs
+// a lane leave registers for 8 blocks, four or eight only for 2 without spills (24688 tokens of
+// 17 heads of 81 elements backward: 205 us with 3 blocks, 147 us with 8).
+constexpr int bwd_blocks(int E, int V) { return E * V <= 2 ? 8 : E <= 2 ? kBwdBlocks : 2; }
+constexpr int fwd_blocks(int E) { return E <= 2 ? kFwdBlocks : 3; }
 constexpr int kFwdRows = 3, kBwdRows = 3;
 constexpr double kInvTwoPi = 0.15915494309189533576888;
 
@@ -142,7 +149,7 @@ template <typename T, int V, int E, bool BWD> struct Ring {
 // lane, `lanes` lanes per row. The first rows are on their way before the angles are taken.
 // Dynamic shared memory: in the backward float[2][h], then the ring of rows.
 template <typename T, int V, int PAIRS, int E, bool BWD>
-__global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks : kFwdBlocks) : 1)
+__global__ void __launch_bounds__(kHeadThreads, BWD ? bwd_blocks(E, V) : fwd_blocks(E))
     head_kernel(HeadArgs a, int log_tile, int lanes) {
   extern __shared__ __align__(16) float acc[];
   // The rows on their way: DEPTH of them in shared memory by asynchronous copies, each thread's
@@ -386,14 +393,16 @@ __global__ void __launch_bounds__(kHeadThreads, E * V <= 8 ? (BWD ? kBwdBlocks :
 }
 
 template <typename T, int V, int PAIRS, int E, bool BWD>
-cudaError_t launch_tiles(const HeadArgs& a, int lanes, cudaStream_t s) {
+cudaError_t launch_tiles(const HeadArgs& a, int lanes, long long* rows, cudaStream_t s) {
   // A token per group, while the tiles still give every SM four blocks.
   const long long M = (long long)a.B * a.N;
   const int groups = kHeadThreads / lanes;
   int log_tile = 0;
   while (2 << log_tile <= groups && (M >> (log_tile + 1)) >= 148 * 4) ++log_tile;
   const long long tiles = (M + (1 << log_tile) - 1) >> log_tile;
-  const long long blocks = BWD ? head_bwd_blocks(a.B, a.N) : tiles;
+  const long long most = 148LL * bwd_blocks(E, V);   // one wave
+  const long long blocks = BWD && tiles > most ? most : tiles;
+  if (rows) *rows = blocks;
   size_t smem = BWD ? (2 * (size_t)a.h * sizeof(float) + 15) / 16 * 16 : 0;
   using L = Ring<T, V, E, BWD>;
   if (L::on) smem += (size_t)L::depth * L::bytes * kHeadThreads;
@@ -402,18 +411,18 @@ cudaError_t launch_tiles(const HeadArgs& a, int lanes, cudaStream_t s) {
 }
 
 template <typename T, int V, int PAIRS, bool BWD>
-cudaError_t launch_runs(const HeadArgs& a, cudaStream_t s) {
+cudaError_t launch_runs(const HeadArgs& a, long long* rows, cudaStream_t s) {
   const int runs = ((a.h + 1) / 2 + V - 1) / V;   // V pairs each
   int lanes = 1;
   while (lanes < 32 && lanes < runs) lanes *= 2;
   const int e = (runs + lanes - 1) / lanes;
-  if (e <= 1) return launch_tiles<T, V, PAIRS, 1, BWD>(a, lanes, s);
+  if (e <= 1) return launch_tiles<T, V, PAIRS, 1, BWD>(a, lanes, rows, s);
   if constexpr (V <= 4)
-    if (e <= 2) return launch_tiles<T, V, PAIRS, 2, BWD>(a, lanes, s);
+    if (e <= 2) return launch_tiles<T, V, PAIRS, 2, BWD>(a, lanes, rows, s);
   if constexpr (V <= 2)
-    if (e <= 4) return launch_tiles<T, V, PAIRS, 4, BWD>(a, lanes, s);
+    if (e <= 4) return launch_tiles<T, V, PAIRS, 4, BWD>(a, lanes, rows, s);
   if constexpr (V <= 1)
-    if (e <= 8) return launch_tiles<T, V, PAIRS, 8, BWD>(a, lanes, s);
+    if (e <= 8) return launch_tiles<T, V, PAIRS, 8, BWD>(a, lanes, rows, s);
   return cudaErrorInvalidValue;
 }
 
@@ -433,32 +442,33 @@ bool fits(const HeadArgs& a, int V, int size) {
 }
 
 template <typename T, int V, bool BWD>
-cudaError_t launch_pairs(const HeadArgs& a, cudaStream_t s) {
-  return a.pairs == PAIRS_HALVES ? launch_runs<T, V, PAIRS_HALVES, BWD>(a, s)
-                                 : launch_runs<T, V, PAIRS_INTERLEAVED, BWD>(a, s);
+cudaError_t launch_pairs(const HeadArgs& a, long long* rows, cudaStream_t s) {
+  return a.pairs == PAIRS_HALVES ? launch_runs<T, V, PAIRS_HALVES, BWD>(a, rows, s)
+                                 : launch_runs<T, V, PAIRS_INTERLEAVED, BWD>(a, rows, s);
 }
 
 template <bool BWD>
-cudaError_t launch(int dt, const HeadArgs& a, cudaStream_t s) {
+cudaError_t launch(int dt, const HeadArgs& a, long long* rows, cudaStream_t s) {
   if (dt == DT_BF16) {
-    if (fits(a, 8, 2)) return launch_pairs<bf16, 8, BWD>(a, s);
-    if (fits(a, 4, 2)) return launch_pairs<bf16, 4, BWD>(a, s);
-    if (fits(a, 2, 2)) return launch_pairs<bf16, 2, BWD>(a, s);
-    return launch_pairs<bf16, 1, BWD>(a, s);
+    if (fits(a, 8, 2)) return launch_pairs<bf16, 8, BWD>(a, rows, s);
+    if (fits(a, 4, 2)) return launch_pairs<bf16, 4, BWD>(a, rows, s);
+    if (fits(a, 2, 2)) return launch_pairs<bf16, 2, BWD>(a, rows, s);
+    return launch_pairs<bf16, 1, BWD>(a, rows, s);
   }
-  if (fits(a, 4, 4)) return launch_pairs<float, 4, BWD>(a, s);
-  if (fits(a, 2, 4)) return launch_pairs<float, 2, BWD>(a, s);
-  return launch_pairs<float, 1, BWD>(a, s);
+  if (fits(a, 4, 4)) return launch_pairs<float, 4, BWD>(a, rows, s);
+  if (fits(a, 2, 4)) return launch_pairs<float, 2, BWD>(a, rows, s);
+  return launch_pairs<float, 1, BWD>(a, rows, s);
 }
 
 }  // namespace
 
-long long head_bwd_blocks(int B, int N) {
-  const long long M = (long long)B * N;
-  return M < 148 * kBwdBlocks ? M : 148 * kBwdBlocks;   // one wave
+long long head_bwd_max_rows(int B, int N) {
+  return std::min<long long>((long long)B * N, 148LL * bwd_blocks(1, 1));
 }
 
-cudaError_t head_fwd(int dt, const HeadArgs& a, cudaStream_t s) { return launch<false>(dt, a, s); }
-cudaError_t head_bwd(int dt, const HeadArgs& a, cudaStream_t s) { return launch<true>(dt, a, s); }
+cudaError_t head_fwd(int dt, const HeadArgs& a, cudaStream_t s) { return launch<false>(dt, a, nullptr, s); }
+cudaError_t head_bwd(int dt, const HeadArgs& a, long long* rows, cudaStream_t s) {
+  return launch<true>(dt, a, rows, s);
+}
 
 }  // namespace ttt

@@ -56,13 +56,13 @@ struct HeadArgs {
   void* out[3];             // forward: [B, H, N, h]
   const void* dout[3];      // backward: [B, H, N, h]
   void* dx[3];              // backward: [B, N, H, h]
-  float* partials;          // backward with weights: head_bwd_blocks() x [2, h]
+  float* partials;          // backward with weights: rows of [2, h], one per block
 };
 
 cudaError_t head_fwd(int dt, const HeadArgs& a, cudaStream_t s);
-cudaError_t head_bwd(int dt, const HeadArgs& a, cudaStream_t s);
-// Blocks of the backward, each with one row [2, h] of partial weight gradients.
-long long head_bwd_blocks(int B, int N);
+// *rows: the rows of partials that the launch writes, at most head_bwd_max_rows().
+cudaError_t head_bwd(int dt, const HeadArgs& a, long long* rows, cudaStream_t s);
+long long head_bwd_max_rows(int B, int N);
 
 // ------------------------------------------------------------------ selective scan
 struct ScanArgs {

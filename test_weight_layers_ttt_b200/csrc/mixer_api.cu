@@ -119,7 +119,7 @@ ttt_status check_heads(const ttt_heads_desc* d, HeadArgs* a) {
 
 size_t plan_heads(const HeadArgs& a, void* base, float** partials) {
   Carve cv(base);
-  *partials = cv.take_n<float>(head_bwd_blocks(a.B, a.N) * 2 * a.h);
+  *partials = cv.take_n<float>(head_bwd_max_rows(a.B, a.N) * 2 * a.h);
   return cv.off;
 }
 
@@ -367,10 +367,11 @@ ttt_status ttt_head_norm_rope_bwd(const ttt_heads_desc* desc, const void* q, con
   return with_checks(s, {{dq, n[0], dt}, {dk, n[1], dt}, {dv, n[2], dt},
                          {dwq, a.h, DT_F32}, {dwk, a.h, DT_F32}}, [&]() -> ttt_status {
     const bool any = M > 0 && a.H[0] + a.H[1] + a.H[2] > 0;
-    if (any) TTT_OP("head_norm_rope_bwd", head_bwd(dt, a, s));
+    long long rows = 0;
+    if (any) TTT_OP("head_norm_rope_bwd", head_bwd(dt, a, &rows, s));
     if (sums)
-      TTT_OP("head_norm_rope_bwd_sum", column_sums(part, any ? head_bwd_blocks(a.B, a.N) : 0,
-                                                   {{dwq, dwk, nullptr}, {a.h, a.h, 0}}, s));
+      TTT_OP("head_norm_rope_bwd_sum",
+             column_sums(part, rows, {{dwq, dwk, nullptr}, {a.h, a.h, 0}}, s));
     return TTT_OK;
   });
 }
