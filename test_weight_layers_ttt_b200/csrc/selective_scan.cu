@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
 // cost S / 8 * 4 bytes per token and channel (8 at S = 16, less than the operands), and their
 // states recomputed are as many as registers hold. Some 25 fp32 operations per state, 2.5
 // exponentials and 15 shuffles, shared memory and scheduler cycles around them: at 4 x 4096
-// tokens of 2048 channels 985 us (260 us marks, 690 us main pass, 35 us joins and sums) against
+// tokens of 2048 channels 980 us (258 us marks, 690 us main pass, 32 us joins and sums) against
 // 115 us of exponentials and some 290 us of fp32 operations; the main pass issues 52 % of the
 // time with the 12 warps per SM that its registers leave.
 
