@@ -345,7 +345,16 @@ def _scratch(ws, nbytes, device):
         return workspace(nbytes, device) if nbytes else None
     if ws.device != device:
         raise ValueError(f"ws must be on {device}, got {ws.device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     return ws
+
+
+def _sizes(*sizes):
+    """The sizes as they are, refused where the descriptor's 32 bits would wrap them."""
+    if max(sizes) > 2**31 - 1:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+    return sizes
 
 
 def _new(t):
@@ -373,7 +382,7 @@ def _conv_desc(x, w, bias, act, state, lens, lead):
     _dense(bias, "bias", (D,), torch.float32, device)
     _dense(state, "state", (lead[0], width - 1, D), x.dtype, device)
     _dense(lens, "lens", (lead[0],), torch.int32, device)
-    return abi.ttt_conv_desc(lead[0], lead[1] if len(lead) > 1 else 1, D, width, _dtype_code(x),
+    return abi.ttt_conv_desc(*_sizes(lead[0], lead[1] if len(lead) > 1 else 1, D, width), _dtype_code(x),
                              _choice(ACTS, act, "act"), _rows(x, "x", lead, (D,), x.dtype, device))
 
 
@@ -450,9 +459,9 @@ def _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs):
     _dense(positions, "positions", (B, N), torch.int32, device)
     rot = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
+        rot, = _sizes(2 * inv_freq.numel())
         _dense(inv_freq, "inv_freq", (rot // 2,), torch.float32, device)
-    return abi.ttt_heads_desc(B, N, H[0], H[1], H[2], h, _dtype_code(some),
+    return abi.ttt_heads_desc(*_sizes(B, N, H[0], H[1], H[2], h), _dtype_code(some),
                               _choice(NORMS, norm, "norm"), rot, _choice(PAIRS, pairs, "pairs"),
                               eps, pos0, row[0], row[1], row[2]), some
 
@@ -508,7 +517,7 @@ def _scan_desc(u, dt, A, Bm, Cm, D, z, dt_bias, softplus, state, lens, lead):
     _dense(dt_bias, "dt_bias", (d,), f32, device)
     _dense(state, "state", (lead[0], d, S), f32, device)
     _dense(lens, "lens", (lead[0],), torch.int32, device)
-    return abi.ttt_scan_desc(lead[0], lead[1] if len(lead) > 1 else 1, d, S, G, _dtype_code(u),
+    return abi.ttt_scan_desc(*_sizes(lead[0], lead[1] if len(lead) > 1 else 1, d, S, G), _dtype_code(u),
                              int(bool(softplus)), 0, _rows(u, "u", lead, (d,), dtype, device),
                              _rows(dt, "dt", lead, (d,), dtype, device),
                              _rows(z, "z", lead, (d,), dtype, device),

@@ -315,3 +315,24 @@ def test_other_strides_are_refused(make, lead, width, text):
     with pytest.raises(ValueError) as ei:
         layer._rows(t, "t", lead, width, t.dtype, t.device)
     assert text in str(ei.value)
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    big, f32 = 2**32 + 1, torch.float32
+    x = torch.empty(1, big, 1, dtype=torch.bfloat16, device="meta")
+    w = torch.empty(4, 1, device="meta")
+    with pytest.raises(ValueError, match="below 2"):
+        layer._conv_desc(x, w, None, "silu", None, None, (1, big))
+    bc = torch.empty(1, big, 1, 1, dtype=torch.bfloat16, device="meta")
+    A = torch.empty(1, 1, dtype=f32, device="meta")
+    with pytest.raises(ValueError, match="below 2"):
+        layer._scan_desc(x, x, A, bc, bc, None, None, None, True, None, None, (1, big))
+    assert layer._sizes(0, 2**31 - 1) == (0, 2**31 - 1)
+
+
+def test_a_workspace_must_span_its_elements():
+    cpu = torch.device("cpu")
+    ws = torch.empty(64, dtype=torch.uint8)
+    assert layer._scratch(ws, 64, cpu) is ws
+    with pytest.raises(ValueError, match="contiguous"):
+        layer._scratch(ws[:1].expand(64), 64, cpu)
