@@ -26,11 +26,15 @@ constexpr int kHeadThreads = 128;
 // head: 162 us with one row ahead in registers, 145 us with 4 blocks of 4 rows, 137 us with 6 of
 // 3; backward at 128: 320 us in registers, 224 us with 3 blocks of 3, 308 us with 4 blocks (spills).
 constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
-// Rows that take narrow accesses have no ring and little in flight per thread; one or two pairs
-// a lane leave registers for 8 blocks, four or eight only for 2 without spills (24688 tokens of
-// 17 heads of 81 elements backward: 205 us with 3 blocks, 147 us with 8).
-constexpr int bwd_blocks(int E, int V) { return E * V <= 2 ? 8 : E <= 2 ? kBwdBlocks : 2; }
-constexpr int fwd_blocks(int E) { return E <= 2 ? kFwdBlocks : 3; }
+// Rows of one-element accesses (V = 1) have little in flight per thread, so their backward takes
+// the blocks that its registers leave room for: 24688 tokens of 17 bf16 heads of 81 elements
+// (E = 2) 205 us with 3 blocks, 143 us with 5, 136 us with 6, 147 us with 8; 6000 tokens of 9
+// heads of 255 (E = 4) 60 us with 2, 47 us with 3, 43 us with 4; of 511 (E = 8) 100 us with 2,
+// 87 us with 3, 118 us with 4, and forward 52 us with 3, 43 us with 4, 49 us with 6.
+constexpr int bwd_blocks(int E, int V) {
+  return E * V == 1 ? 8 : E * V == 2 ? 6 : E == 4 && V == 1 ? 4 : kBwdBlocks;
+}
+constexpr int fwd_blocks(int E) { return E < 8 ? kFwdBlocks : 4; }
 constexpr int kFwdRows = 3, kBwdRows = 3;
 constexpr double kInvTwoPi = 0.15915494309189533576888;
 
