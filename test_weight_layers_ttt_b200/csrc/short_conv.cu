@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
       rows.take(0, i, cur);           // zeros behind the sequence's end
       rows.take(1, i, g[0]);
       fetch(i, s + kRing);
-      if (a.act) {
+      if (a.act && s < se) {          // behind the end g is 0, and stays it for an infinite window
         float pre[V];
         fma_v<V>(pre, w[0], cur, bias);
 #pragma unroll
@@ -271,10 +271,12 @@ __global__ void __launch_bounds__(kConvThreads) conv_bwd_kernel(ConvArgs a, int 
       }
       const int t = s - (K - 1);      // the row of dx that g[s] completes
       if (s < s1 && (t >= t0 || r == 0)) {
-        float o[V];
-        mul_v<V>(o, w[0], g[K - 1]);
+        float o[V] = {};              // rows behind the sequence's end
+        if (t < n) {
+          mul_v<V>(o, w[0], g[K - 1]);
 #pragma unroll
-        for (int j = 1; j < K; ++j) fma_v<V>(o, w[j], g[K - 1 - j], o);
+          for (int j = 1; j < K; ++j) fma_v<V>(o, w[j], g[K - 1 - j], o);
+        }
         const int i_out = t + K - 1 - n;   // the row of dstate_out that this row became
         if (a.dstate_out && i_out >= 0 && i_out < K - 1) {
           float f[V];
