@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kHeadThreads, BWD ? bwd_blocks(E, V) : fwd_blo
       if (a.norm != TTT_NORM_NONE) {
         const float s = sum_v<V>(ss), d = BWD ? sum_v<V>(dot) : 0.0f;
         r = rsqrtf(fmaf(group_sum(s, lanes), inv_h, a.eps));
-        if (BWD) back = -r * r * r * group_sum(d, lanes) * inv_h;
+        if (BWD) back = -r * group_sum(d, lanes) * inv_h;
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -338,14 +338,15 @@ __global__ void __launch_bounds__(kHeadThreads, BWD ? bwd_blocks(E, V) : fwd_blo
           fma_v<V>(oa, u, cs[e], oa);
           fma_v<V>(ob, v, cs[e], ob);
         } else {
-          // dx = r (g w) - x r^3 <g w, x> [/ h];  dw += g (x r)
-          mul_v<V>(oa, xa[e], back);
-          mul_v<V>(ob, xb[e], back);
-          fma_v<V>(oa, gwa[e], r, oa);
-          fma_v<V>(ob, gwb[e], r, ob);
+          // dx = r (g w - n r <g w, x> [/ h]) with n = x r, for r^3 leaves fp32's range where eps
+          // and the row are small;  dw += g n
+          mul_v<V>(u, xa[e], r);
+          mul_v<V>(v, xb[e], r);
+          fma_v<V>(oa, u, back, gwa[e]);
+          fma_v<V>(ob, v, back, gwb[e]);
+          mul_v<V>(oa, oa, r);
+          mul_v<V>(ob, ob, r);
           if (a.partials) {
-            mul_v<V>(u, xa[e], r);
-            mul_v<V>(v, xb[e], r);
             if (kind == 0) {
               fma_v<V>(dw[0][e][0], ga[e], u, dw[0][e][0]);
               fma_v<V>(dw[0][e][1], gb[e], v, dw[0][e][1]);

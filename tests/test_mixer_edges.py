@@ -39,3 +39,33 @@ def test_short_conv_gradients_behind_the_end_are_zeros_for_infinite_weights():
     wg[1, 2] = INF
     got = layer.short_conv_bwd(xg, wg, dev(rand(rng, 1, 20, 16)), **g)
     assert float(got[0][0, 11:].abs().sum()) == 0.0
+
+
+# ----------------------------------------------------------------------------- heads
+@pytest.mark.parametrize("dtype,h,rot", [("fp32", 64, 32), ("fp32", 33, 20), ("bf16", 128, 128), ("bf16", 81, 0)])
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+@pytest.mark.parametrize("weight", [True, False])
+def test_head_norm_backward_of_tiny_rows_with_a_small_eps(dtype, h, rot, norm, weight):
+    """dx = r (g - n <g, n>) with n = x r, r up to eps^(-1/2): in range where r^3 is not."""
+    eps, td = float(np.float32(1e-30)), torch_dtype(dtype)
+    rng = np.random.default_rng(33)
+    x, do = rand(rng, 1, 4, 3, h, dtype=dtype), rand(rng, 1, 3, 4, h, dtype=dtype)
+    x[0, 1, 1] = 0.0
+    x[0, 2] = host(dev(x[0, 2] * 1e-15, td))        # of eps' size
+    x[0, 3] = host(dev(x[0, 3] * 1e-19, td))        # far below it
+    w = rand(rng, h) + 1 if weight else None
+    inv = (10000.0 ** (-np.arange(rot // 2) / max(1, rot // 2))).astype(np.float32) if rot else None
+    kw = dict(norm=norm, eps=eps, inv_freq=None if inv is None else dev(inv))
+    got = layer.head_norm_rope_bwd(dev(x, td), None, None, dev(do, td), None, None,
+                                   wq=None if w is None else dev(w), **kw)
+    pos = np.arange(4)[None]
+    dx, dw = M.head_norm_rope_backward(x, do, w, norm, eps, inv, pos)
+    # the terms of a row's dx are at most r sqrt(h) max |g| (Cauchy-Schwarz, either norm), each with
+    # two sums over h and some roundings; |R^T dout| <= 2 max |dout|
+    sq = (x * x).sum(-1)
+    r = 1 / np.sqrt((sq if norm == "l2" else sq / h) + eps)
+    g = 2 * np.abs(do).max() * (1.0 if w is None else np.abs(w).max())
+    for t in range(4):
+        near(got[0][:, t], dx[:, t], 4 * h + 64, f"token {t}", terms=np.sqrt(h) * g * r[0, t].max())
+    if weight:
+        near(got[3], dw, 12 + h + 64, "dw", terms=12 * np.sqrt(h) * g)
