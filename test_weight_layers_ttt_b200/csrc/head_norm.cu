@@ -40,6 +40,11 @@ constexpr double kInvTwoPi = 0.15915494309189533576888;
 
 enum : int { PAIRS_HALVES = 0, PAIRS_INTERLEAVED = 1 };
 
+// The backward without a norm has kernels of its own: its dx does not depend on x, which may be
+// infinite, and a branch in the common kernel costs 3 % (65536 tokens of 3 x 8 heads of 128: 226
+// us, 232 us with it).
+enum Pass { FWD, BWD_NORMED, BWD_PLAIN };
+
 // First and second element of pair `p`: rotated pairs first, then the elements behind `rot`
 // paired the same way (the last pair of an odd h has no second element).
 template <int PAIRS>
@@ -152,9 +157,10 @@ template <typename T, int V, int E, bool BWD> struct Ring {
 // neighbouring groups write neighbouring rows of the head-major output. E runs of V pairs per
 // lane, `lanes` lanes per row. The first rows are on their way before the angles are taken.
 // Dynamic shared memory: in the backward float[2][h], then the ring of rows.
-template <typename T, int V, int PAIRS, int E, bool BWD>
-__global__ void __launch_bounds__(kHeadThreads, BWD ? bwd_blocks(E, V) : fwd_blocks(E))
+template <typename T, int V, int PAIRS, int E, Pass P>
+__global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fwd_blocks(E))
     head_kernel(HeadArgs a, int log_tile, int lanes) {
+  constexpr bool BWD = P != FWD, NORMED = P == BWD_NORMED;
   extern __shared__ __align__(16) float acc[];
   // The rows on their way: DEPTH of them in shared memory by asynchronous copies, each thread's
   // own, where an access has the 4 bytes that such a copy takes at least; else one in registers.
@@ -318,7 +324,7 @@ __global__ void __launch_bounds__(kHeadThreads, BWD ? bwd_blocks(E, V) : fwd_blo
           fma_v<V>(dot, gwb[e], xb[e], dot);
         }
       }
-      if (a.norm != TTT_NORM_NONE) {
+      if (BWD ? NORMED : a.norm != TTT_NORM_NONE) {
         const float s = sum_v<V>(ss), d = BWD ? sum_v<V>(dot) : 0.0f;
         r = rsqrtf(fmaf(group_sum(s, lanes), inv_h, a.eps));
         if (BWD) back = -r * group_sum(d, lanes) * inv_h;
@@ -342,10 +348,12 @@ __global__ void __launch_bounds__(kHeadThreads, BWD ? bwd_blocks(E, V) : fwd_blo
           // and the row are small;  dw += g n
           mul_v<V>(u, xa[e], r);
           mul_v<V>(v, xb[e], r);
-          fma_v<V>(oa, u, back, gwa[e]);
-          fma_v<V>(ob, v, back, gwb[e]);
-          mul_v<V>(oa, oa, r);
-          mul_v<V>(ob, ob, r);
+          if constexpr (NORMED) {
+            fma_v<V>(gwa[e], u, back, gwa[e]);
+            fma_v<V>(gwb[e], v, back, gwb[e]);
+          }
+          mul_v<V>(oa, gwa[e], r);
+          mul_v<V>(ob, gwb[e], r);
           if (a.partials) {
             if (kind == 0) {
               fma_v<V>(dw[0][e][0], ga[e], u, dw[0][e][0]);
@@ -397,8 +405,9 @@ __global__ void __launch_bounds__(kHeadThreads, BWD ? bwd_blocks(E, V) : fwd_blo
   }
 }
 
-template <typename T, int V, int PAIRS, int E, bool BWD>
+template <typename T, int V, int PAIRS, int E, Pass P>
 cudaError_t launch_tiles(const HeadArgs& a, int lanes, long long* rows, cudaStream_t s) {
+  constexpr bool BWD = P != FWD;
   // A token per group, while the tiles still give every SM four blocks.
   const long long M = (long long)a.B * a.N;
   const int groups = kHeadThreads / lanes;
@@ -411,23 +420,23 @@ cudaError_t launch_tiles(const HeadArgs& a, int lanes, long long* rows, cudaStre
   size_t smem = BWD ? (2 * (size_t)a.h * sizeof(float) + 15) / 16 * 16 : 0;
   using L = Ring<T, V, E, BWD>;
   if (L::on) smem += (size_t)L::depth * L::bytes * kHeadThreads;
-  head_kernel<T, V, PAIRS, E, BWD><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, log_tile, lanes);
+  head_kernel<T, V, PAIRS, E, P><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, log_tile, lanes);
   return cudaGetLastError();
 }
 
-template <typename T, int V, int PAIRS, bool BWD>
+template <typename T, int V, int PAIRS, Pass P>
 cudaError_t launch_runs(const HeadArgs& a, long long* rows, cudaStream_t s) {
   const int runs = ((a.h + 1) / 2 + V - 1) / V;   // V pairs each
   int lanes = 1;
   while (lanes < 32 && lanes < runs) lanes *= 2;
   const int e = (runs + lanes - 1) / lanes;
-  if (e <= 1) return launch_tiles<T, V, PAIRS, 1, BWD>(a, lanes, rows, s);
+  if (e <= 1) return launch_tiles<T, V, PAIRS, 1, P>(a, lanes, rows, s);
   if constexpr (V <= 4)
-    if (e <= 2) return launch_tiles<T, V, PAIRS, 2, BWD>(a, lanes, rows, s);
+    if (e <= 2) return launch_tiles<T, V, PAIRS, 2, P>(a, lanes, rows, s);
   if constexpr (V <= 2)
-    if (e <= 4) return launch_tiles<T, V, PAIRS, 4, BWD>(a, lanes, rows, s);
+    if (e <= 4) return launch_tiles<T, V, PAIRS, 4, P>(a, lanes, rows, s);
   if constexpr (V <= 1)
-    if (e <= 8) return launch_tiles<T, V, PAIRS, 8, BWD>(a, lanes, rows, s);
+    if (e <= 8) return launch_tiles<T, V, PAIRS, 8, P>(a, lanes, rows, s);
   return cudaErrorInvalidValue;
 }
 
@@ -446,23 +455,23 @@ bool fits(const HeadArgs& a, int V, int size) {
   return true;
 }
 
-template <typename T, int V, bool BWD>
+template <typename T, int V, Pass P>
 cudaError_t launch_pairs(const HeadArgs& a, long long* rows, cudaStream_t s) {
-  return a.pairs == PAIRS_HALVES ? launch_runs<T, V, PAIRS_HALVES, BWD>(a, rows, s)
-                                 : launch_runs<T, V, PAIRS_INTERLEAVED, BWD>(a, rows, s);
+  return a.pairs == PAIRS_HALVES ? launch_runs<T, V, PAIRS_HALVES, P>(a, rows, s)
+                                 : launch_runs<T, V, PAIRS_INTERLEAVED, P>(a, rows, s);
 }
 
-template <bool BWD>
+template <Pass P>
 cudaError_t launch(int dt, const HeadArgs& a, long long* rows, cudaStream_t s) {
   if (dt == DT_BF16) {
-    if (fits(a, 8, 2)) return launch_pairs<bf16, 8, BWD>(a, rows, s);
-    if (fits(a, 4, 2)) return launch_pairs<bf16, 4, BWD>(a, rows, s);
-    if (fits(a, 2, 2)) return launch_pairs<bf16, 2, BWD>(a, rows, s);
-    return launch_pairs<bf16, 1, BWD>(a, rows, s);
+    if (fits(a, 8, 2)) return launch_pairs<bf16, 8, P>(a, rows, s);
+    if (fits(a, 4, 2)) return launch_pairs<bf16, 4, P>(a, rows, s);
+    if (fits(a, 2, 2)) return launch_pairs<bf16, 2, P>(a, rows, s);
+    return launch_pairs<bf16, 1, P>(a, rows, s);
   }
-  if (fits(a, 4, 4)) return launch_pairs<float, 4, BWD>(a, rows, s);
-  if (fits(a, 2, 4)) return launch_pairs<float, 2, BWD>(a, rows, s);
-  return launch_pairs<float, 1, BWD>(a, rows, s);
+  if (fits(a, 4, 4)) return launch_pairs<float, 4, P>(a, rows, s);
+  if (fits(a, 2, 4)) return launch_pairs<float, 2, P>(a, rows, s);
+  return launch_pairs<float, 1, P>(a, rows, s);
 }
 
 }  // namespace
@@ -471,9 +480,9 @@ long long head_bwd_max_rows(int B, int N) {
   return std::min<long long>((long long)B * N, 148LL * bwd_blocks(1, 1));
 }
 
-cudaError_t head_fwd(int dt, const HeadArgs& a, cudaStream_t s) { return launch<false>(dt, a, nullptr, s); }
+cudaError_t head_fwd(int dt, const HeadArgs& a, cudaStream_t s) { return launch<FWD>(dt, a, nullptr, s); }
 cudaError_t head_bwd(int dt, const HeadArgs& a, long long* rows, cudaStream_t s) {
-  return launch<true>(dt, a, rows, s);
+  return a.norm == TTT_NORM_NONE ? launch<BWD_PLAIN>(dt, a, rows, s) : launch<BWD_NORMED>(dt, a, rows, s);
 }
 
 }  // namespace ttt

@@ -69,3 +69,17 @@ def test_head_norm_backward_of_tiny_rows_with_a_small_eps(dtype, h, rot, norm, w
         near(got[0][:, t], dx[:, t], 4 * h + 64, f"token {t}", terms=np.sqrt(h) * g * r[0, t].max())
     if weight:
         near(got[3], dw, 12 + h + 64, "dw", terms=12 * np.sqrt(h) * g)
+
+
+@pytest.mark.parametrize("dtype,h,rot,pairs", [("fp32", 64, 64, "halves"), ("bf16", 80, 40, "interleaved"),
+                                               ("fp32", 7, 0, "halves")])
+def test_head_gradients_without_a_norm_do_not_depend_on_the_input(dtype, h, rot, pairs):
+    td = torch_dtype(dtype)
+    rng = np.random.default_rng(34)
+    x, do = rand(rng, 2, 5, 2, h, dtype=dtype), rand(rng, 2, 2, 5, h, dtype=dtype)
+    inv = dev((10000.0 ** (-np.arange(rot // 2) / max(1, rot // 2))).astype(np.float32)) if rot else None
+    xg, dg = dev(x, td), dev(do, td)
+    ref = layer.head_norm_rope_bwd(xg, None, None, dg, None, None, norm=None, inv_freq=inv, pairs=pairs)[0]
+    xg[0, 1, 1, 2], xg[1, 4, 0, 5], xg[1, 0, 0] = INF, float("nan"), -INF
+    got = layer.head_norm_rope_bwd(xg, None, None, dg, None, None, norm=None, inv_freq=inv, pairs=pairs)[0]
+    assert torch.equal(got, ref)
