@@ -157,7 +157,7 @@ template <typename T, int V, int E, bool BWD> struct Ring {
 // neighbouring groups write neighbouring rows of the head-major output. E runs of V pairs per
 // lane, `lanes` lanes per row. The first rows are on their way before the angles are taken.
 // Dynamic shared memory: in the backward float[2][h], then the ring of rows.
-template <typename T, int V, int PAIRS, int E, Pass P>
+template <typename T, int V, int PAIRS, int E, Pass P, bool ALL>
 __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fwd_blocks(E))
     head_kernel(HeadArgs a, int log_tile, int lanes) {
   constexpr bool BWD = P != FWD, NORMED = P == BWD_NORMED;
@@ -188,6 +188,15 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
     for (int q = 0; q < V; ++q) dw[0][e][0][q] = dw[0][e][1][q] = dw[1][e][0][q] = dw[1][e][1][q] = 0.0f;
   }
 
+  // What a pair's elements add to each other is nothing behind the rotated ones, not 0 times an
+  // element that may be infinite. ALL: there are none behind, or one, which is alone.
+  const auto rotated_only = [&](int e, float (&u)[V], float (&v)[V]) {
+    if constexpr (!ALL) {
+#pragma unroll
+      for (int q = 0; q < V; ++q)
+        if ((e * lanes + lane) * V + q >= half) u[q] = v[q] = 0.0f;
+    }
+  };
   for (long long tile0 = (long long)blockIdx.x << log_tile; tile0 < M; tile0 += (long long)gridDim.x << log_tile) {
     const long long m = tile0 + (group & ((1 << log_tile) - 1));
     const bool live = m < M;
@@ -309,6 +318,7 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
           float u[V], v[V];
           mul_v<V>(u, ga[e], ns[e]);
           mul_v<V>(v, gb[e], sn[e]);
+          rotated_only(e, u, v);
           fma_v<V>(ga[e], ga[e], cs[e], v);
           fma_v<V>(gb[e], gb[e], cs[e], u);
 #pragma unroll
@@ -341,6 +351,7 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
           }
           mul_v<V>(oa, v, ns[e]);
           mul_v<V>(ob, u, sn[e]);
+          rotated_only(e, oa, ob);
           fma_v<V>(oa, u, cs[e], oa);
           fma_v<V>(ob, v, cs[e], ob);
         } else {
@@ -420,7 +431,8 @@ cudaError_t launch_tiles(const HeadArgs& a, int lanes, long long* rows, cudaStre
   size_t smem = BWD ? (2 * (size_t)a.h * sizeof(float) + 15) / 16 * 16 : 0;
   using L = Ring<T, V, E, BWD>;
   if (L::on) smem += (size_t)L::depth * L::bytes * kHeadThreads;
-  head_kernel<T, V, PAIRS, E, P><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, log_tile, lanes);
+  if (a.rot + 1 >= a.h) head_kernel<T, V, PAIRS, E, P, true><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, log_tile, lanes);
+  else head_kernel<T, V, PAIRS, E, P, false><<<(unsigned)blocks, kHeadThreads, smem, s>>>(a, log_tile, lanes);
   return cudaGetLastError();
 }
 

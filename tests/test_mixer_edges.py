@@ -83,3 +83,27 @@ def test_head_gradients_without_a_norm_do_not_depend_on_the_input(dtype, h, rot,
     xg[0, 1, 1, 2], xg[1, 4, 0, 5], xg[1, 0, 0] = INF, float("nan"), -INF
     got = layer.head_norm_rope_bwd(xg, None, None, dg, None, None, norm=None, inv_freq=inv, pairs=pairs)[0]
     assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("h,rot", [(64, 32), (80, 20), (96, 0), (33, 20), (128, 6)])
+@pytest.mark.parametrize("pairs", ["halves", "interleaved"])
+def test_elements_behind_the_rotation_stay_apart(dtype, h, rot, pairs):
+    """Without a norm an element behind the rotated ones is passed on alone, forward and backward:
+    an infinite neighbour does not reach it."""
+    td = torch_dtype(dtype)
+    rng = np.random.default_rng(35)
+    x = dev(rand(rng, 2, 3, 2, h, dtype=dtype), td)
+    inv = dev((10000.0 ** (-np.arange(rot // 2) / max(1, rot // 2))).astype(np.float32)) if rot else None
+    kw = dict(norm=None, inv_freq=inv, pairs=pairs, pos0=5)
+    for at in (rot, rot + (h - rot) // 2, h - 1):
+        bad = x.clone()
+        bad[1, 2, 0, at] = INF
+        want = layer.head_norm_rope_fwd(x, None, **kw)[0]
+        want[1, 0, 2, at] = INF
+        assert torch.equal(layer.head_norm_rope_fwd(bad, None, **kw)[0], want)
+        do = x.transpose(1, 2).contiguous()
+        want = layer.head_norm_rope_bwd(x, None, None, do, None, None, **kw)[0]
+        want[1, 2, 0, at] = INF
+        do[1, 0, 2, at] = INF
+        assert torch.equal(layer.head_norm_rope_bwd(x, None, None, do, None, None, **kw)[0], want)
