@@ -107,7 +107,7 @@ ttt_status check_heads(const ttt_heads_desc* d, HeadArgs* a) {
   if (d->h > 512) return fail(TTT_ERR_UNSUPPORTED, "h must be <= 512");
   if (d->Hq > 65535 || d->Hk > 65535 || d->Hv > 65535)
     return fail(TTT_ERR_UNSUPPORTED, "Hq, Hk and Hv must be <= 65535");
-  if (d->pos0 < 0 || d->pos0 > INT_MAX) return fail(TTT_ERR_INVALID_ARG, "pos0 must be in 0..2^31-1");
+  if (d->pos0 < 0) return fail(TTT_ERR_INVALID_ARG, "pos0 must be >= 0");
   *a = HeadArgs{};
   a->B = d->B; a->N = d->N; a->h = d->h; a->norm = d->norm; a->rot = d->rot; a->pairs = d->pairs;
   a->eps = d->eps; a->pos0 = d->pos0;

@@ -442,6 +442,8 @@ def short_conv_bwd(x, w, dy, *, bias=None, act="silu", state=None, lens=None, ds
 
 
 def _heads_desc(q, k, v, wq, wk, norm, eps, inv_freq, positions, pos0, pairs):
+    if not 0 <= pos0 < 2**31:       # the descriptor's 32 bits would wrap it
+        raise ValueError(f"pos0 must be in 0..2^31-1, got {pos0}")
     some = next((t for t in (q, k, v) if t is not None), None)
     if some is None:
         raise ValueError("one of q, k and v must be given")

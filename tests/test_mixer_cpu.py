@@ -336,3 +336,15 @@ def test_a_workspace_must_span_its_elements():
     assert layer._scratch(ws, 64, cpu) is ws
     with pytest.raises(ValueError, match="contiguous"):
         layer._scratch(ws[:1].expand(64), 64, cpu)
+
+
+@pytest.mark.parametrize("pos0", [2**31, 2**32 + 5, -1, -2**32 + 5])
+def test_positions_beyond_32_bits_are_refused(pos0):
+    """In front of every other check, for the descriptor's 32 bits would wrap them."""
+    q = torch.empty(1, 2, 1, 8)
+    for call in (lambda: layer.head_norm_rope_fwd(q, None, pos0=pos0),
+                 lambda: layer.head_norm_rope_bwd(q, None, None, q, None, None, pos0=pos0)):
+        with pytest.raises(ValueError, match="pos0"):
+            call()
+    with pytest.raises(ValueError, match="CUDA"):
+        layer.head_norm_rope_fwd(q, None, pos0=2**31 - 1)
