@@ -23,6 +23,7 @@
 // state), scan_join carries the states over the chunks, and the outputs pass starts every chunk
 // from its state. That doubles the exponentials, so it is done only for few channels.
 #include <algorithm>
+#include <cfloat>
 
 #include "mixer.h"
 #include "mixer_common.cuh"
@@ -40,6 +41,11 @@ __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// A for exp2, kept finite: a padded token's step of 0 times it is 0, and its decay 1.
+__device__ __forceinline__ float log2_rate(float A) {
+  const float a = A * kLog2e;
+  return a < -FLT_MAX ? -FLT_MAX : a;
 }
 // exp2(d a) for the recurrences. Just below 0, where slow decays live, the hardware's result is
 // low by 0.6e-8 to 2.7e-8 in the mean (measured), which a recurrence with a memory of 1000
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(kFwdThreads) scan_fwd_kernel(ScanArgs a, int b
     for (int i = 0; i < M; ++i) {
       const int s = sl * M + i;
       const bool on = mine && s < a.S;
-      v[i] = on ? a.A[(long long)c * a.S + s] * kLog2e : 0.0f;
+      v[i] = on ? log2_rate(a.A[(long long)c * a.S + s]) : 0.0f;
       if (OUT && a.chunks > 1) w[i] = mine ? a.ends[at + i] : 0.0f;
       else if (OUT && a.state_in) w[i] = on ? a.state_in[io + s] : 0.0f;
     }
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(256) scan_join_kernel(ScanArgs a, int SP) {
     const long long bd = i / SP;
     const int d = (int)(bd % a.D), b = (int)(bd / a.D);
     const bool on = s < a.S;
-    const float A2 = on ? a.A[(long long)d * a.S + s] * kLog2e : 0.0f;
+    const float A2 = on ? log2_rate(a.A[(long long)d * a.S + s]) : 0.0f;
     const float* first = back ? a.dstate_out : a.state_in;
     float* io = back ? a.back : a.ends;
     float h = on && first ? first[bd * a.S + s] : 0.0f;
@@ -466,13 +472,15 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
       if (s0 + k < a.S) A4[k] = A[s0 + k];
   }
 #pragma unroll
+  for (int k = 0; k < 4; ++k) A4[k] = log2_rate(A4[k]);
+#pragma unroll
   for (int j = 0; j < NB; ++j) {
     delta[j] += bias;
     if (a.softplus) delta[j] = softplus(delta[j]);
     float y = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      h[j][k] = fmaf(ex2(fmaf(delta[j], A4[k] * kLog2e, kExpBias)), h[j][k], delta[j] * u[j] * B4[j][k]);
+      h[j][k] = fmaf(ex2(fmaf(delta[j], A4[k], kExpBias)), h[j][k], delta[j] * u[j] * B4[j][k]);
       y = fmaf(h[j][k], C4[j][k], y);
     }
     const bool live = on && b0 + j < a.B;
@@ -542,7 +550,7 @@ __global__ void __launch_bounds__(kFwdThreads) scan_marks_kernel(ScanArgs a, int
     const int s = sl * M + 2 * i;
     const float lo = mine && s < a.S ? a.A[(long long)c * a.S + s] : 0.0f;
     const float hi = mine && s + 1 < a.S ? a.A[(long long)c * a.S + s + 1] : 0.0f;
-    A2[i] = pack2(lo * kLog2e, hi * kLog2e);
+    A2[i] = pack2(log2_rate(lo), log2_rate(hi));
     h[i] = share[i] = 0;
     prod[i] = both(1.0f);
   }
@@ -732,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) scan_bwd_kernel(ScanArg
       const int s = sl * 4 + i;
       const bool on = c + z < r.c1 && s < a.S;
       const long long io = ((long long)b * a.D + c + z) * a.S + s;
-      v[i] = on ? a.A[(long long)(c + z) * a.S + s] * kLog2e : 0.0f;
+      v[i] = on ? log2_rate(a.A[(long long)(c + z) * a.S + s]) : 0.0f;
       if (on && a.chunks == 1) {        // one piece: nothing was joined
         w[i] = a.state_in ? a.state_in[io] : 0.0f;
         g[i] = a.dstate_out ? a.dstate_out[io] : 0.0f;

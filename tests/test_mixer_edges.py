@@ -107,3 +107,41 @@ def test_elements_behind_the_rotation_stay_apart(dtype, h, rot, pairs):
         want[1, 2, 0, at] = INF
         do[1, 0, 2, at] = INF
         assert torch.equal(layer.head_norm_rope_bwd(x, None, None, do, None, None, **kw)[0], want)
+
+
+# ----------------------------------------------------------------------------- selective scan
+@pytest.mark.parametrize("value", [-3e38, -INF])
+@pytest.mark.parametrize("N,lens", [(37, None), (37, [37, 20]), (300, [299, 45]), (300, [0, 1])])
+def test_a_decay_beyond_the_range_of_its_exponent_forgets_at_once(value, N, lens):
+    """exp(delta A) = 0 for each of a sequence's tokens; the padded tokens of a tile and whole pieces
+    behind the end step by 0."""
+    S, D = 16, 24
+    h, g, rng = scan_case("fp32", 2, N, D, S, 1, True, True, lens, True, 0, seed=36)
+    dy, ds = rand(rng, 2, N, D), rand(rng, 2, D, S)
+    h["A"][3, 5] = h["A"][10] = -1e30               # as good as infinite: delta > 1e-3 here
+    g["A"][3, 5] = g["A"][10] = value
+    y, st = layer.selective_scan_fwd(**g)
+    ry, hs = M.selective_scan(**h)
+    near(y, ry, scan_roundings(N, S), "y")
+    near(st, hs[:, -1], scan_roundings(N, S), "state")
+    if value != -INF:                               # the gradient of delta has the factor A
+        got = layer.selective_scan_bwd(**g, dy=dev(dy), dstate=dev(ds))
+        ref = M.selective_scan_backward(**h, dy=dy, dstate=ds)
+        for t, name in zip(got, ("du", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dstate")):
+            near(t, ref[name], 2 * scan_roundings(N, S) + 2 * N + D, name)
+
+
+def test_a_step_takes_a_decay_beyond_the_range_of_its_exponent():
+    h, g, _ = scan_case("fp32", 3, 1, 10, 16, 1, True, True, None, True, 0, seed=37)
+    h["A"][2] = -1e30
+    g["A"][2] = -3e38
+    ry, hs = M.selective_scan(**h)
+    g.pop("softplus")
+    one = {k: v[:, 0].contiguous() if k in ("u", "dt", "z", "Bm", "Cm") else v for k, v in g.items()}
+    near(layer.selective_scan_step(**one), ry[:, 0], scan_roundings(1, 16))
+    near(one["state"], hs[:, -1], scan_roundings(1, 16))
+    # a step of zero is no decay
+    g["dt"].zero_(), g["dt_bias"].zero_()
+    one["dt"], before = one["dt"].zero_(), one["state"].clone()
+    layer.selective_scan_step(**one, softplus=False)
+    assert torch.equal(one["state"], before)
