@@ -516,6 +516,7 @@ ttt_status ttt_selective_scan_step(const ttt_scan_desc* desc, const void* u, con
  * the gradient of state_out) give du, ddt [B,N,D], dA [D,S] fp32, dBm, dCm [B,N,G,S], dz (with
  * z) [B,N,D], and dD, ddt_bias (nullable) [D] and dstate_in (nullable) [B,D,S] fp32. The
  * states are recomputed. workspace >= ttt_selective_scan_workspace_bytes(desc, 1) bytes.
+ * A channel whose state becomes infinite or NaN may have NaN in its dA, whichever token did it.
  */
 ttt_status ttt_selective_scan_bwd(const ttt_scan_desc* desc, const void* u, const void* dt,
                                   const float* A, const void* Bm, const void* Cm, const float* D,

@@ -145,3 +145,23 @@ def test_a_step_takes_a_decay_beyond_the_range_of_its_exponent():
     one["dt"], before = one["dt"].zero_(), one["state"].clone()
     layer.selective_scan_step(**one, softplus=False)
     assert torch.equal(one["state"], before)
+
+
+@pytest.mark.parametrize("dtype,N,n,D,S", [("fp32", 60, 45, 40, 16), ("bf16", 300, 130, 64, 16),
+                                           ("fp32", 30, 30, 18, 33), ("bf16", 300, 300, 9, 8)])
+def test_an_infinite_last_input_reaches_no_gradient_in_front_of_it(dtype, N, n, D, S):
+    """The last token's u is in its own state, output and gradients only: du (which is without u) and
+    what other tokens and channels have stay what they are. Its own channel's dA is a sum that it
+    may spoil, as it does those of dD and ddt_bias."""
+    _, g, rng = scan_case(dtype, 2, N, D, S, 1, True, True, [n, max(n - 9, 0)], True, 0, seed=38)
+    dy = dev(rand(rng, 2, N, D, dtype=dtype), torch_dtype(dtype))
+    ref = layer.selective_scan_bwd(**g, dy=dy)
+    g["u"][0, n - 1, 4] = INF
+    got = layer.selective_scan_bwd(**g, dy=dy)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[8], ref[8])
+    for i in (1, 3, 4, 6):                           # ddt, dB, dC, dz of all other tokens
+        ref[i][0, n - 1], got[i][0, n - 1] = 0, 0
+        assert torch.equal(got[i], ref[i])
+    for i in (2, 5, 7):                              # dA, dD, ddt_bias of all other channels
+        ref[i][4], got[i][4] = 0, 0
+        assert torch.equal(got[i], ref[i])
