@@ -188,14 +188,21 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
     for (int q = 0; q < V; ++q) dw[0][e][0][q] = dw[0][e][1][q] = dw[1][e][0][q] = dw[1][e][1][q] = 0.0f;
   }
 
-  // What a pair's elements add to each other is nothing behind the rotated ones, not 0 times an
-  // element that may be infinite. ALL: there are none behind, or one, which is alone.
-  const auto rotated_only = [&](int e, float (&u)[V], float (&v)[V]) {
+  // (x, y) -> (x cos + y s, y cos + x t). Behind the rotated pairs x and y stay as they are, for 0
+  // times an infinite neighbour is NaN (ALL: there are none behind, or one, which is alone). Selects
+  // and no skip: 30000 tokens of 24 bf16 heads of 128, half of it rotated, 68.7 us against 72.6 us.
+  const auto rotate = [&](int e, float (&x)[V], float (&y)[V], const float (&c)[V], const float (&s)[V],
+                          const float (&t)[V]) {
+    float u[V], v[V];
+    mul_v<V>(u, x, t);
+    mul_v<V>(v, y, s);
     if constexpr (!ALL) {
 #pragma unroll
       for (int q = 0; q < V; ++q)
         if ((e * lanes + lane) * V + q >= half) u[q] = v[q] = 0.0f;
     }
+    fma_v<V>(x, x, c, v);
+    fma_v<V>(y, y, c, u);
   };
   for (long long tile0 = (long long)blockIdx.x << log_tile; tile0 < M; tile0 += (long long)gridDim.x << log_tile) {
     const long long m = tile0 + (group & ((1 << log_tile) - 1));
@@ -315,12 +322,7 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
         fma_v<V>(ss, xa[e], xa[e], ss);
         fma_v<V>(ss, xb[e], xb[e], ss);
         if (BWD) {   // the rotation's transpose, then the weights
-          float u[V], v[V];
-          mul_v<V>(u, ga[e], ns[e]);
-          mul_v<V>(v, gb[e], sn[e]);
-          rotated_only(e, u, v);
-          fma_v<V>(ga[e], ga[e], cs[e], v);
-          fma_v<V>(gb[e], gb[e], cs[e], u);
+          rotate(e, ga[e], gb[e], cs[e], sn[e], ns[e]);
 #pragma unroll
           for (int q = 0; q < V; ++q) {
             gwa[e][q] = ga[e][q];
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
       }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        float oa[V], ob[V], u[V], v[V];
+        float u[V], v[V];
         if constexpr (!BWD) {
           mul_v<V>(u, xa[e], r);
           mul_v<V>(v, xb[e], r);
@@ -349,11 +351,8 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
             mul_v<V>(u, u, wa[e]);
             mul_v<V>(v, v, wb[e]);
           }
-          mul_v<V>(oa, v, ns[e]);
-          mul_v<V>(ob, u, sn[e]);
-          rotated_only(e, oa, ob);
-          fma_v<V>(oa, u, cs[e], oa);
-          fma_v<V>(ob, v, cs[e], ob);
+          rotate(e, u, v, cs[e], ns[e], sn[e]);
+          write(e, u, v);
         } else {
           // dx = r (g w - n r <g w, x> [/ h]) with n = x r, for r^3 leaves fp32's range where eps
           // and the row are small;  dw += g n
@@ -363,8 +362,9 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
             fma_v<V>(gwa[e], u, back, gwa[e]);
             fma_v<V>(gwb[e], v, back, gwb[e]);
           }
-          mul_v<V>(oa, gwa[e], r);
-          mul_v<V>(ob, gwb[e], r);
+          mul_v<V>(gwa[e], gwa[e], r);
+          mul_v<V>(gwb[e], gwb[e], r);
+          write(e, gwa[e], gwb[e]);
           if (a.partials) {
             if (kind == 0) {
               fma_v<V>(dw[0][e][0], ga[e], u, dw[0][e][0]);
@@ -375,7 +375,6 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
             }
           }
         }
-        write(e, oa, ob);
       }
       out.next(a, first, step, BWD ? minor_step : major_step, 0, target);
     }
