@@ -34,7 +34,10 @@ constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
 constexpr int bwd_blocks(int E, int V) {
   return E * V == 1 ? 8 : E * V == 2 ? 6 : E == 4 && V == 1 ? 4 : kBwdBlocks;
 }
-constexpr int fwd_blocks(int E) { return E < 8 ? kFwdBlocks : 4; }
+// Forward, heads of which a part is rotated (`all` false): 69 registers where all has 64, so the 8
+// blocks that those leave room for are asked for (17 heads of 81, none of it rotated: 89 us, 92 us
+// without; with whole rotation 42 us at 2 x 6172 tokens of 16 heads, 43 us if it is asked for).
+constexpr int fwd_blocks(int E, int V, bool all) { return !all && V == 1 && E <= 2 ? 8 : E < 8 ? kFwdBlocks : 4; }
 constexpr int kFwdRows = 3, kBwdRows = 3;
 constexpr double kInvTwoPi = 0.15915494309189533576888;
 
@@ -158,7 +161,7 @@ template <typename T, int V, int E, bool BWD> struct Ring {
 // lane, `lanes` lanes per row. The first rows are on their way before the angles are taken.
 // Dynamic shared memory: in the backward float[2][h], then the ring of rows.
 template <typename T, int V, int PAIRS, int E, Pass P, bool ALL>
-__global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fwd_blocks(E))
+__global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fwd_blocks(E, V, ALL))
     head_kernel(HeadArgs a, int log_tile, int lanes) {
   constexpr bool BWD = P != FWD, NORMED = P == BWD_NORMED;
   extern __shared__ __align__(16) float acc[];
@@ -189,14 +192,17 @@ __global__ void __launch_bounds__(kHeadThreads, P != FWD ? bwd_blocks(E, V) : fw
   }
 
   // (x, y) -> (x cos + y s, y cos + x t). Behind the rotated pairs x and y stay as they are, for 0
-  // times an infinite neighbour is NaN (ALL: there are none behind, or one, which is alone). Selects
-  // and no skip: 30000 tokens of 24 bf16 heads of 128, half of it rotated, 68.7 us against 72.6 us.
+  // times an infinite neighbour is NaN (ALL: there are none behind, or one, which is alone). Lanes of
+  // one pair skip the rotation (2 x 6172 tokens of 16 bf16 heads of 66, 20 of it rotated: 43.4 us,
+  // 44.0 us with selects), runs of pairs select (30000 tokens of 24 heads of 128, half of it rotated:
+  // 68.7 us, 72.6 us with a skip).
   const auto rotate = [&](int e, float (&x)[V], float (&y)[V], const float (&c)[V], const float (&s)[V],
                           const float (&t)[V]) {
+    if (!ALL && V == 1 && (e * lanes + lane) * V >= half) return;
     float u[V], v[V];
     mul_v<V>(u, x, t);
     mul_v<V>(v, y, s);
-    if constexpr (!ALL) {
+    if constexpr (!ALL && V > 1) {
 #pragma unroll
       for (int q = 0; q < V; ++q)
         if ((e * lanes + lane) * V + q >= half) u[q] = v[q] = 0.0f;
