@@ -366,11 +366,13 @@ ttt_status ttt_lm_target(int32_t N, int32_t d, const void* X0, const float* conv
  * the state is the one after the sequence's last token.
  *
  * Outputs may not overlap inputs or one another, except that a forward's state_out may be its
- * state_in. Sums, norms, states and all elementwise math are fp32; 16-bit outputs are rounded
- * once. Results are the same on every call with the same arguments (no atomics). Nothing is
- * kept between calls; the calls can be captured into a CUDA graph. Errors, streams and
- * ownership as for the rest of the library; the debug checks cover these calls too
- * (ttt_debug_check_workspace excepted, which takes a ttt_desc).
+ * state_in. Sums, norms, states and all elementwise math are fp32, for fp32 tensors too: sigmoid
+ * and silu come from the hardware's exponential and reciprocal (relative error of some 1e-7
+ * (1 + |x|)), decays from its exponential. 16-bit outputs are rounded once. Results are the
+ * same on every call with the same arguments (no atomics). Nothing is kept between calls; the
+ * calls can be captured into a CUDA graph. Errors, streams and ownership as for the rest of the
+ * library; the debug checks cover these calls too (ttt_debug_check_workspace excepted, which
+ * takes a ttt_desc).
  * ------------------------------------------------------------------------------------ */
 enum { TTT_ACT_NONE = 0, TTT_ACT_SILU = 1 };
 enum { TTT_NORM_NONE = 0, TTT_NORM_RMS = 1, TTT_NORM_L2 = 2 };

@@ -10,8 +10,9 @@
 // shuffle sum. The angles of a token are the same for all its heads: a group keeps one token
 // and its lanes the cosines and sines of their pairs in registers, each taken once, from a
 // 64-bit product (fp32 loses far positions: 1e6 * 2^-24 is 0.06 of a radian) reduced to
-// [-1/2, 1/2] turns. 2 x 32768 tokens of 3 x 4 heads of 256: 138 us, 5.8 TB/s, 89 % of the
-// measured copy rate; 65536 tokens of 3 x 8 heads of 128 backward: 223 us, 74 %.
+// [-1/2, 1/2] turns. 2 x 32768 tokens of 3 x 4 heads of 256: 144 to 152 us on different cards, 5.3
+// to 5.6 TB/s, 81 to 85 % of the measured copy rate; 65536 tokens of 3 x 8 heads of 128 backward:
+// 219 to 226 us, 73 to 75 %.
 #include <algorithm>
 
 #include "mixer.h"
@@ -25,9 +26,11 @@ constexpr int kHeadThreads = 128;
 // and rows that each thread has on their way. Two lm-sized tensors' forward of 256 elements a
 // head: 162 us with one row ahead in registers, 145 us with 4 blocks of 4 rows, 137 us with 6 of
 // 3; backward at 128: 320 us in registers, 224 us with 3 blocks of 3, 308 us with 4 blocks (spills).
+// Forward pairs in halves of more than 256 elements that are not whole 16-byte runs spill 24 to 86
+// bytes with 6.
 constexpr int kFwdBlocks = 6, kBwdBlocks = 3;
 // Rows of one-element accesses (V = 1) have little in flight per thread, so their backward takes
-// the blocks that its registers leave room for: 24688 tokens of 17 bf16 heads of 81 elements
+// the blocks that its registers leave room for (figures of the time): 24688 tokens of 17 bf16 heads of 81 elements
 // (E = 2) 205 us with 3 blocks, 143 us with 5, 136 us with 6, 147 us with 8; 6000 tokens of 9
 // heads of 255 (E = 4) 60 us with 2, 47 us with 3, 43 us with 4; of 511 (E = 8) 100 us with 2,
 // 87 us with 3, 118 us with 4, and forward 52 us with 3, 43 us with 4, 49 us with 6.

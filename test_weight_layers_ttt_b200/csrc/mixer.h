@@ -33,7 +33,7 @@ struct ConvArgs {
   const void* dstate_out;   // [B, width - 1, D] or null
   void* dx;
   void* dstate_in;          // or null
-  float* partials;          // backward: conv_bwd_partials() floats
+  float* partials;          // backward: conv_bwd_rows() rows of [width + 1, D]
 };
 
 cudaError_t conv_fwd(int dt, const ConvArgs& a, cudaStream_t s);

@@ -6,8 +6,8 @@
 // What bounds it: one exponential per (token, channel, state) - 16 per token and channel at
 // the usual S = 16 - against 16 exponentials per clock and SM (measured; the fp32 pipe does 125
 // operations, two-wide or not). That is 231 us for 8 x 2048 tokens of 4096 channels, where HBM
-// needs 82 us. The kernel takes 447 us: the exponential unit is busy 61 % of it, the shared
-// memory pipe 69 %, the schedulers 58 %, so what is left is their overlap.
+// needs 82 us. The kernel takes 447 us: the exponential unit is busy 62 % of it, the shared
+// memory pipe 71 %, the schedulers 60 %, so what is left is their overlap.
 //
 // Layout: a lane keeps 4 states of one channel (2 channels in the backward) in registers, packed
 // in pairs for the two-wide fp32 instructions, which halves the issue slots; SL lanes share a
@@ -512,11 +512,11 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(ScanArgs a) {
 // The states are recomputed, not saved: the first pass leaves a mark (the state from the
 // chunk's zero) every 8 tokens and the main pass walks the marks backwards. Marks of 8 tokens
 // cost S / 8 * 4 bytes per token and channel (8 at S = 16, less than the operands), and their
-// states recomputed are as many as registers hold. Some 25 fp32 operations per state, 2.5
-// exponentials and 15 shuffles, shared memory and scheduler cycles around them: at 4 x 4096
-// tokens of 2048 channels 980 us (258 us marks, 690 us main pass, 32 us joins and sums) against
-// 115 us of exponentials and some 290 us of fp32 operations; the main pass issues 52 % of the
-// time with the 12 warps per SM that its registers leave.
+// states recomputed are as many as registers hold. Some 25 fp32 operations and 2.5 exponentials
+// per state, 7 shuffles per token of a lane (8 states), shared memory and scheduler cycles around
+// them: at 4 x 4096 tokens of 2048 channels 980 us (258 us marks, 690 us main pass, 32 us joins and
+// sums) against 115 us of exponentials and some 290 us of fp32 operations; the main pass issues 53 %
+// of the time with the 12 warps per SM that its registers leave.
 
 // Marks, chunk end states, and with more than one chunk the chunk's share of the state gradient
 // in front of it, sum_t (prod_{t' <= t} a_t') C_t g_t. Same tiling as the forward.
@@ -702,7 +702,8 @@ __device__ __forceinline__ int mark_slot(int ch, int sl) {
 // Of the 8 tokens only 4 at a time hold their a_t and h_t in registers: the first 4 are run
 // through once for the state in front of the last 4, and again when their turn comes. That is
 // half an exponential more per state, and three blocks per SM instead of two (1251 us against
-// 1322 us at the time, both sides without spills; 2 tokens at a time, four blocks and 1.75
+// 1322 us at the time, both sides without spills; not for S <= 8, whose shared memory of 79 KB in
+// bf16 and 96 KB in fp32 leaves room for two, and which spill 12 bytes; 2 tokens at a time, four blocks and 1.75
 // exponentials 702 to 753 us against 700 us). A token's operands are read, and its channel
 // sums shuffled, a token apart from their use (756 -> 698 us). VEC: the next 8 tokens' operands
 // come by asynchronous copies under this one's arithmetic; else through registers, two blocks.
@@ -1268,7 +1269,8 @@ int scan_channel_blocks(int D, int G, int S) {
 }
 
 // Blocks to fill the card with: two rounds of those that run at a time (148 SMs x 7 forward, x 3
-// backward; one round: 400 us against 387 us forward for 32768 tokens of 1024 channels, 990 us
+// backward, counted for bf16, aligned, S <= 16 and used for all: fp32 and more states have 4 or 5
+// forward, odd channels 2 backward; one round: 400 us against 387 us forward for 32768 tokens of 1024 channels, 990 us
 // against 980 us backward for the sizes above, three rounds 394 us and 990 us), and the tokens'
 // worth of work that starting and joining a chunk costs (8, 24 and 40 gave the same times; 64
 // fewer and worse balanced chunks, 1203 us against 1100 us backward at the time). The forward's

@@ -4,11 +4,14 @@
 // HBM bound: a token costs one read and one write of its channels forward, two reads and one
 // write backward. A thread owns V consecutive channels over a run of tokens and slides the
 // window through registers, so a row is read once per run (plus width - 1 halo rows) and every
-// access of the vector form is 8 or 16 bytes. kRing rows are on their way while one is used:
-// bytes in flight set the rate (2 rows 74 us, 4 rows 58 us, 8 rows 56 us forward and 74 us
-// against 70 us backward); the arithmetic is two-wide. 2 x 32768 tokens of 1024 channels, width
-// 4, silu, bf16: 60 us forward, 4.5 TB/s; the exponential unit, two results per silu, is busy 58 %
-// of it. 4 x 4096 tokens of 2048 channels backward: 63 us, 61 % of the issue slots.
+// access of the vector form is 8 or 16 bytes. kRing rows are on their way while one is used
+// (when the ring came 2 rows took 74 us, 4 rows 58 us, 8 rows 56 us forward, and 4 rows 70 us, 8
+// rows 74 us backward); the arithmetic is two-wide. 2 x 32768 tokens of 1024 channels, width 4,
+// silu, bf16: 59 us forward, 4.5 TB/s, the exponential unit (two results per silu) busy 60 % of it
+// and the issue slots 51 %; 4 x 4096 tokens of 2048 channels backward: 59 us with the column sums,
+// 63 % of the issue slots. Neither is full: both launch 1024 blocks, of which the registers (96 and
+// 95) let 5 run on an SM, 1.38 rounds of them. Few channels leave the column sums to few blocks: 16
+// x 32768 tokens of 8 channels backward take 248 us, 100 us of it the sums.
 #include "mixer.h"
 #include "mixer_common.cuh"
 
