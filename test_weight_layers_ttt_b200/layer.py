@@ -8,6 +8,8 @@ eta [B,H,N] fp32; W0, W2 [H,h,m] fp32 ([H,m,h] with w_in_layout=1); W1 [H,m,h] f
 The token-mixer operators (short_conv_*, head_norm_rope_*, selective_scan_*) take token-major
 inputs [B,N,...] that may be slices of a wider projection (one stride between all tokens);
 they run on the device of their first tensor, on its current stream unless ``stream`` is given.
+A caller who gives one orders it behind the streams that made the inputs, and keeps the inputs
+until it is done; the outputs belong to it.
 """
 from __future__ import annotations
 
